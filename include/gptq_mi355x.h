@@ -66,7 +66,7 @@ typedef enum {
 #define GPTQ_NOALLOC_MAX_WEIGHTS (1 << 24)
 #define GPTQ_NOALLOC_MAX_ROWS 65536
 
-typedef enum { GPTQ_F16 = 0, GPTQ_F32 = 1 } gptq_dtype;
+typedef enum { GPTQ_F16 = 0, GPTQ_F32 = 1, GPTQ_BF16 = 2 /* key-value cache entry points only */ } gptq_dtype;
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* gptq_status_string(int status);
@@ -343,6 +343,123 @@ int gptq_gather(const void* src, int elem_bytes, int64_t src_rows, int64_t src_c
 int gptq_dequant_matvec(const uint32_t* packed, const float* scales, const int32_t* zeros,
                         int64_t d_row, int64_t d_col, int bits, int64_t group_size, const void* x,
                         int64_t batch, int64_t ldx, float* y, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Quantised key-value cache: generation with a packed model keeps the keys
+ * and values of its attention layers in 4 or 8 bits, too.
+ *
+ * Defines: What = s (code - z) (astro-blog survey, section 1.2) on the
+ * min-max grid of gptq_quantize_layer (aiqz.cc, section 分组方案), one group
+ * per token and key-value head:
+ *   lo = min(0, min x), hi = max(0, max x), s = (hi - lo) / (2^bits - 1),
+ *   z = rint(-lo / s), code = clamp(rint(x / s) + z, 0, 2^bits - 1).
+ * hi - lo and s are fp32 operations; s is then rounded to 16 significant
+ * bits (ties to even), and rint (ties to even) is taken of the real
+ * quotients by that s. A vector whose s would be below 2^-126 takes the
+ * grid of [-1, 1] and reads as zeros. A vector with an infinity or a NaN, or
+ * whose hi - lo is not finite, reads as NaN.
+ *
+ * The cache is paged. Its buffers are the caller's, 16-byte aligned, all on
+ * the device; the two structs are host memory, read during the call.
+ *   k_codes, v_codes  uint32 [n_pages][kv_heads][page_size][head_dim * bits / 32]:
+ *            the codes of a token's head, packed as in `packed` above.
+ *   k_grid, v_grid    uint32 [n_pages][kv_heads][page_size]: the grid word
+ *            of a token's head, the fp32 bits of s with z in the low 8 bits.
+ *   page_size         a power of two, 16 to 1024 tokens.
+ *   head_dim          a multiple of 16, 16 to 256.
+ *   bits              4 or 8.
+ * A batch names the sequences and the tokens that a call deals with, always
+ * the last ones of their sequences:
+ *   table    int32 [batch] rows ld_table apart: entry i of a row is the page
+ *            of positions i * page_size and on; max_pages entries a row.
+ *            Entries past a sequence's length are not read.
+ *   lens     int32 [batch]: tokens of each sequence, with those of the call.
+ *   starts   int32 [batch + 1], not decreasing: the call's rows starts[b] ..
+ *            starts[b + 1] - 1 are the last tokens of sequence b; NULL: one
+ *            token a sequence (n_tokens == batch).
+ *   n_tokens rows of the call. Rows past starts[batch] are left as they are.
+ * A row whose position lies before its sequence's start (lens[b] smaller
+ * than the sequence's rows: an idle place of the batch has lens[b] = 0 or
+ * less) has no token. Pages may be shared between sequences that are only
+ * read; the positions that one gptq_kv_cache_write stores have to lie in
+ * different places of the cache (a place that is written twice is left with
+ * a mixture).
+ *   info     device int32 or NULL: set to 1 if a position lies past the
+ *            table or on a page outside 0 .. n_pages - 1, else left as it
+ *            is, so that one word can collect over many calls. Nothing is
+ *            read or written there.
+ * Shared errors: NULL structs, buffers, table or lens; buffers not aligned;
+ * page_size, head_dim or bits other than above; n_pages outside 1 .. 2^31 - 1,
+ * kv_heads outside 1 .. 65535, batch or n_tokens outside 0 .. 2^25, max_pages
+ * outside 1 .. 2^31 - 1, ld_table < max_pages; starts NULL and n_tokens !=
+ * batch -> GPTQ_E_INVALID_ARG. n_tokens = 0 or batch = 0 does nothing.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  uint32_t* k_codes;
+  uint32_t* v_codes;
+  uint32_t* k_grid;
+  uint32_t* v_grid;
+  int64_t n_pages;
+  int64_t page_size;
+  int64_t kv_heads;
+  int64_t head_dim;
+  int bits;
+} gptq_kv_cache;
+
+typedef struct {
+  const int32_t* table;
+  int64_t ld_table;
+  int64_t max_pages;
+  const int32_t* lens;
+  const int32_t* starts;
+  int64_t batch;
+  int64_t n_tokens;
+} gptq_kv_batch;
+
+/* Stores the call's tokens: k and v are n_tokens rows of kv_heads x head_dim
+ * elements (GPTQ_F16, GPTQ_BF16 or GPTQ_F32), rows ldk and ldv elements
+ * apart. Rows without a token, or on no page, are skipped.
+ * Errors: the shared ones; ldk or ldv < kv_heads * head_dim or > 2^40, NULL or
+ * unaligned k or v, unknown dtype -> GPTQ_E_INVALID_ARG. */
+int gptq_kv_cache_write(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const void* k, const void* v,
+                        int dtype, int64_t ldk, int64_t ldv, int32_t* info, void* stream);
+
+/* Reads the call's tokens back: k and v receive s (code - z), computed in
+ * fp32 and rounded to dtype. Rows without a token, or on no page, are
+ * written as zeros. Arguments and errors as for gptq_kv_cache_write. */
+int gptq_kv_cache_read(const gptq_kv_cache* cache, const gptq_kv_batch* batch, void* k, void* v, int dtype,
+                       int64_t ldk, int64_t ldv, int32_t* info, void* stream);
+
+/* Attention of the call's tokens over their sequences' cached tokens, their
+ * own among them (store them first):
+ *   out[t][h] = sum_j p_j v_j / sum_j p_j,  j = 0 .. pos_t,
+ *   p_j = exp(scale q[t][h].k_j + slopes[h] (j - pos_t))
+ * with pos_t the token's position and key-value head h / (q_heads /
+ * kv_heads). A row that sees no key is written as zeros; keys on no page are
+ * left out.
+ *   q        device, n_tokens rows of q_heads x head_dim elements (GPTQ_F16,
+ *            GPTQ_BF16 or GPTQ_F32), rows ldq apart; q_heads a multiple of
+ *            kv_heads.
+ *   slopes   device fp32 [q_heads] or NULL (none): linear position biases.
+ *   out      device, n_tokens rows like q's, of out_dtype, rows ldo apart;
+ *            must not overlap q.
+ *   ws       device, 16-byte aligned, of gptq_kv_attention_workspace_size
+ *            bytes (0 bytes: may be NULL). The size does not depend on what
+ *            lens, starts and the table hold.
+ * Sums and softmax statistics are fp32. Weights enter the second product as
+ * fp16 with a common scale per row (error 2^-11 of a weight); with an fp32 q
+ * or out both products take their operand in two fp16 parts (2^-22). Results
+ * are deterministic. Queries that are not finite give NaN rows.
+ * Errors: the shared ones; q_heads < 1, > 65535 or no multiple of kv_heads,
+ * ldq or ldo < q_heads * head_dim or > 2^40, NULL or unaligned q or out,
+ * unaligned slopes or ws, scale not finite in fp32, unknown dtype, 2^24 or more
+ * workgroups (kv_heads times the 16-row blocks of the call's query rows) ->
+ * GPTQ_E_INVALID_ARG; ws_bytes too small -> GPTQ_E_WORKSPACE. The workspace
+ * size is 0 for arguments that would be refused. */
+size_t gptq_kv_attention_workspace_size(const gptq_kv_cache* cache, const gptq_kv_batch* batch, int64_t q_heads);
+int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const void* q, int q_dtype,
+                      int64_t q_heads, int64_t ldq, double scale, const float* slopes, void* out, int out_dtype,
+                      int64_t ldo, void* ws, size_t ws_bytes, int32_t* info, void* stream);
 
 /* ------------------------------------------------------------------------
  * Packing of existing codes (the same device routine the sweep uses).

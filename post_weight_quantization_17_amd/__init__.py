@@ -22,11 +22,22 @@ LIB_PATH = os.path.join(_PKG, "libgptq_mi355x.so")
 
 GPTQ_OK, GPTQ_E_INVALID_ARG, GPTQ_E_UNSUPPORTED, GPTQ_E_WORKSPACE, GPTQ_E_HIP, GPTQ_E_TOO_LARGE = range(6)
 GPTQ_NOALLOC_MAX_WEIGHTS, GPTQ_NOALLOC_MAX_ROWS = 1 << 24, 65536
-GPTQ_F16, GPTQ_F32 = 0, 1
+GPTQ_F16, GPTQ_F32, GPTQ_BF16 = 0, 1, 2
 
 _lib: Optional[ctypes.CDLL] = None
 
 _c_size, _c_i64, _c_int, _c_dbl, _c_ptr = ctypes.c_size_t, ctypes.c_int64, ctypes.c_int, ctypes.c_double, ctypes.c_void_p
+
+
+class _KvCacheStruct(ctypes.Structure):  # gptq_kv_cache
+    _fields_ = [("k_codes", _c_ptr), ("v_codes", _c_ptr), ("k_grid", _c_ptr), ("v_grid", _c_ptr), ("n_pages", _c_i64),
+                ("page_size", _c_i64), ("kv_heads", _c_i64), ("head_dim", _c_i64), ("bits", _c_int)]
+
+
+class _KvBatchStruct(ctypes.Structure):  # gptq_kv_batch
+    _fields_ = [("table", _c_ptr), ("ld_table", _c_i64), ("max_pages", _c_i64), ("lens", _c_ptr), ("starts", _c_ptr),
+                ("batch", _c_i64), ("n_tokens", _c_i64)]
+
 
 _SIGNATURES = {
     "gptq_status_string": (ctypes.c_char_p, [_c_int]),
@@ -57,6 +68,14 @@ _SIGNATURES = {
          _c_size, _c_ptr],
     ),
     "gptq_dequant_gemm_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "gptq_kv_cache_write": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_i64, _c_i64, _c_ptr, _c_ptr]),
+    "gptq_kv_cache_read": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_i64, _c_i64, _c_ptr, _c_ptr]),
+    "gptq_kv_attention_workspace_size": (_c_size, [_c_ptr, _c_ptr, _c_i64]),
+    "gptq_kv_attention": (
+        _c_int,
+        [_c_ptr, _c_ptr, _c_ptr, _c_int, _c_i64, _c_i64, _c_dbl, _c_ptr, _c_ptr, _c_int, _c_i64, _c_ptr, _c_size, _c_ptr,
+         _c_ptr],
+    ),
     "gptq_dequant_matvec": (
         _c_int,
         [_c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_int, _c_i64, _c_ptr, _c_i64, _c_i64, _c_ptr, _c_ptr],
@@ -479,3 +498,205 @@ def gptq_dequant_gemm(packed: torch.Tensor, scales: torch.Tensor, zeros: torch.T
                               ldx, _ptr(Y), ldy, int(bool(relu)), wsp, wsb, _stream()),
     )
     return Y
+
+
+# ------------------------------------------------- quantised key-value cache
+@dataclasses.dataclass
+class KVCache:
+    """A paged cache of 4- or 8-bit keys and values (``gptq_kv_cache_alloc``
+    makes one). ``info`` collects over all calls on the cache: it becomes 1
+    when a call met a position past its table or on no page of the cache."""
+
+    k_codes: torch.Tensor  # int32 view of the uint32 words [n_pages, kv_heads, page_size, head_dim*bits/32]
+    v_codes: torch.Tensor
+    k_grid: torch.Tensor  # int32 view of the grid words [n_pages, kv_heads, page_size]: fp32 scale | zero
+    v_grid: torch.Tensor
+    head_dim: int
+    bits: int
+    info: torch.Tensor  # int32 [1] (device)
+
+
+def gptq_kv_cache_alloc(n_pages: int, page_size: int, kv_heads: int, head_dim: int, bits: int, device) -> KVCache:
+    """A zero-filled cache of n_pages pages of page_size tokens."""
+    if bits not in (4, 8):
+        raise ValueError("bits must be 4 or 8")
+    if head_dim % 16 != 0 or not 16 <= head_dim <= 256:
+        raise ValueError("head_dim must be a multiple of 16, 16 to 256")
+    if page_size & (page_size - 1) or not 16 <= page_size <= 1024:
+        raise ValueError("page_size must be a power of two, 16 to 1024")
+    if n_pages < 1 or kv_heads < 1:
+        raise ValueError("n_pages and kv_heads must be at least 1")
+    rows = (n_pages, kv_heads, page_size)
+    z = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)
+    return KVCache(k_codes=z(*rows, head_dim * bits // 32), v_codes=z(*rows, head_dim * bits // 32), k_grid=z(*rows),
+                   v_grid=z(*rows), head_dim=head_dim, bits=bits, info=z(1))
+
+
+def _kv_structs(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, starts: Optional[torch.Tensor],
+                n_tokens: int):
+    """The two structs of a call, after the checks of shapes and devices."""
+    dev = cache.k_codes.device
+    tensors = [("cache.k_codes", cache.k_codes), ("cache.v_codes", cache.v_codes), ("cache.k_grid", cache.k_grid),
+               ("cache.v_grid", cache.v_grid), ("cache.info", cache.info), ("table", table), ("lens", lens)]
+    if starts is not None:
+        tensors.append(("starts", starts))
+    for name, t in tensors:
+        _on_gpu(name, t)
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
+        if t.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32")
+        if name != "table" and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    grid = cache.k_grid.shape
+    if len(grid) != 3 or cache.v_grid.shape != grid:
+        raise ValueError("cache grids must be [n_pages, kv_heads, page_size]")
+    codes = (*grid, cache.head_dim * cache.bits // 32)
+    if cache.k_codes.shape != codes or cache.v_codes.shape != codes:
+        raise ValueError("cache codes must be [n_pages, kv_heads, page_size, head_dim * bits / 32]")
+    if cache.info.numel() != 1:
+        raise ValueError("cache.info must hold one element")
+    if lens.dim() != 1:
+        raise ValueError("lens must be a vector")
+    batch = lens.shape[0]
+    if table.dim() != 2 or table.shape[0] != batch or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("table must be [batch, max_pages] with unit column stride")
+    if starts is not None and starts.shape != (batch + 1,):
+        raise ValueError("starts must be [batch + 1]")
+    if starts is None and n_tokens != batch:
+        raise ValueError("without starts there is one token a sequence")
+    c = _KvCacheStruct(_ptr(cache.k_codes), _ptr(cache.v_codes), _ptr(cache.k_grid), _ptr(cache.v_grid), grid[0],
+                       grid[2], grid[1], cache.head_dim, cache.bits)
+    ld = table.stride(0) if batch > 1 else table.shape[1]
+    b = _KvBatchStruct(_ptr(table), ld, table.shape[1], _ptr(lens), _ptr(starts), batch, n_tokens)
+    return c, b
+
+
+def _kv_dtype(name: str, dtype: torch.dtype) -> int:
+    codes = {torch.float16: GPTQ_F16, torch.float32: GPTQ_F32, torch.bfloat16: GPTQ_BF16}
+    if dtype not in codes:
+        raise TypeError(f"{name}: unsupported dtype {dtype} (float16, bfloat16 or float32)")
+    return codes[dtype]
+
+
+def _kv_rows(name: str, t: torch.Tensor, n: Optional[int], heads: Optional[int], dim: int, dev) -> int:
+    """Checks [n_tokens, heads, dim] with heads and elements contiguous; returns the token stride."""
+    _on_gpu(name, t)
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
+    if (t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads)
+            or (n is not None and t.shape[0] != n)):
+        raise ValueError(f"{name} must be [n_tokens, heads, head_dim] of the call and its cache")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name} must have its heads and their elements contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * dim
+
+
+def gptq_kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                        starts: Optional[torch.Tensor] = None) -> None:
+    """Quantise and store k, v [n_tokens, kv_heads, head_dim] (fp16, bf16 or
+    fp32; rows may be strided) as the last tokens of their sequences:
+    ``lens`` [batch] counts each sequence's tokens with these, rows
+    ``starts[b]:starts[b + 1]`` are sequence b's (None: one each), ``table``
+    [batch, max_pages] holds its pages."""
+    dev = cache.k_codes.device
+    n = k.shape[0]
+    c, b = _kv_structs(cache, table, lens, starts, n)
+    heads = cache.k_grid.shape[1]
+    ldk, ldv = (_kv_rows(name, t, n, heads, cache.head_dim, dev) for name, t in (("k", k), ("v", v)))
+    if v.dtype != k.dtype:
+        raise ValueError("k and v must have the same dtype")
+    lib = load()
+    with torch.cuda.device(dev):
+        _check("gptq_kv_cache_write",
+               lib.gptq_kv_cache_write(ctypes.byref(c), ctypes.byref(b), _ptr(k), _ptr(v), _kv_dtype("k", k.dtype), ldk,
+                                       ldv, _ptr(cache.info), _stream()))
+
+
+def gptq_kv_cache_read(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, starts: Optional[torch.Tensor] = None,
+                       n_tokens: Optional[int] = None, dtype: torch.dtype = torch.float16, out=None):
+    """(k, v) [n_tokens, kv_heads, head_dim]: what the cache holds of the
+    last tokens of the sequences (arguments as in gptq_kv_cache_write;
+    ``n_tokens`` rows in all, needed with ``starts`` unless ``out`` = (k, v)
+    is given). Rows past ``starts[batch]`` are left as they are (unspecified
+    in new tensors)."""
+    dev = cache.k_codes.device
+    heads = cache.k_grid.shape[1]
+    if out is None:
+        if n_tokens is None:
+            if starts is not None:
+                raise ValueError("n_tokens is needed with starts")
+            n_tokens = lens.shape[0]
+        out = tuple(torch.empty((n_tokens, heads, cache.head_dim), dtype=dtype, device=dev) for _ in range(2))
+    k, v = out
+    n = k.shape[0]
+    if n_tokens is not None and n_tokens != n:
+        raise ValueError("out has another number of rows than n_tokens")
+    c, b = _kv_structs(cache, table, lens, starts, n)
+    ldk, ldv = (_kv_rows(name, t, n, heads, cache.head_dim, dev) for name, t in (("k", k), ("v", v)))
+    if v.dtype != k.dtype:
+        raise ValueError("k and v must have the same dtype")
+    lib = load()
+    with torch.cuda.device(dev):
+        _check("gptq_kv_cache_read",
+               lib.gptq_kv_cache_read(ctypes.byref(c), ctypes.byref(b), _ptr(k), _ptr(v), _kv_dtype("out", k.dtype),
+                                      ldk, ldv, _ptr(cache.info), _stream()))
+    return k, v
+
+
+def gptq_kv_attention_workspace_size(cache: KVCache, table: torch.Tensor, n_tokens: int, q_heads: int,
+                                     ragged: Optional[bool] = None) -> int:
+    """Bytes of workspace that gptq_kv_attention takes for n_tokens rows of
+    q_heads heads over the sequences of ``table`` (``ragged``: with starts;
+    None: the larger of both where both are possible)."""
+    grid = cache.k_grid.shape
+    c = _KvCacheStruct(_ptr(cache.k_codes), _ptr(cache.v_codes), _ptr(cache.k_grid), _ptr(cache.v_grid), grid[0],
+                       grid[2], grid[1], cache.head_dim, cache.bits)
+    lib = load()
+    sizes = []
+    p = _ptr(table)
+    for r in (True, False) if ragged is None else (ragged,):
+        if r or n_tokens == table.shape[0]:
+            b = _KvBatchStruct(p, table.shape[1], table.shape[1], p, p if r else None, table.shape[0], n_tokens)
+            sizes.append(lib.gptq_kv_attention_workspace_size(ctypes.byref(c), ctypes.byref(b), q_heads))
+    return max(sizes, default=0)
+
+
+def gptq_kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor,
+                      starts: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                      slopes: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None,
+                      out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out [n_tokens, q_heads, head_dim] (``dtype``, by default q's): causal
+    attention of q [n_tokens, q_heads, head_dim] (fp16, bf16 or fp32) over
+    the cached tokens of its sequences, its own among them. ``scale``: by
+    default 1 / sqrt(head_dim); ``slopes`` fp32 [q_heads]: linear position
+    biases. Rows past ``starts[batch]`` are left as they are (unspecified in
+    a new tensor)."""
+    dev = cache.k_codes.device
+    n = q.shape[0]
+    c, b = _kv_structs(cache, table, lens, starts, n)
+    ldq = _kv_rows("q", q, n, None, cache.head_dim, dev)
+    hq = q.shape[1]
+    if hq % cache.k_grid.shape[1] != 0:
+        raise ValueError("q's heads must be a multiple of the cache's")
+    if slopes is not None:
+        _on_gpu("slopes", slopes)
+        if slopes.device != dev or slopes.dtype != torch.float32 or slopes.shape != (hq,) or not slopes.is_contiguous():
+            raise ValueError("slopes must be a contiguous float32 [q_heads] vector on the cache's device")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype if dtype is None else dtype, device=dev)
+    elif dtype is not None and out.dtype != dtype:
+        raise ValueError("out has another dtype than asked for")
+    ldo = _kv_rows("out", out, n, hq, cache.head_dim, dev)
+    lib = load()
+    with torch.cuda.device(dev):
+        need = lib.gptq_kv_attention_workspace_size(ctypes.byref(c), ctypes.byref(b), hq)
+        if ws is not None and (ws.device != dev or not ws.is_contiguous()):
+            raise ValueError("ws must be contiguous and on the cache's device")
+        ws = _workspace(need, dev, ws)
+        _check("gptq_kv_attention",
+               lib.gptq_kv_attention(ctypes.byref(c), ctypes.byref(b), _ptr(q), _kv_dtype("q", q.dtype), hq, ldq,
+                                     cache.head_dim ** -0.5 if scale is None else float(scale), _ptr(slopes), _ptr(out),
+                                     _kv_dtype("out", out.dtype), ldo, _ptr(ws), ws.numel() * ws.element_size(),
+                                     _ptr(cache.info), _stream()))
+    return out
