@@ -501,11 +501,12 @@ def gptq_dequant_gemm(packed: torch.Tensor, scales: torch.Tensor, zeros: torch.T
 
 
 # ------------------------------------------------- quantised key-value cache
-@dataclasses.dataclass
+@dataclasses.dataclass(frozen=True, eq=False)
 class KVCache:
     """A paged cache of 4- or 8-bit keys and values (``gptq_kv_cache_alloc``
     makes one). ``info`` collects over all calls on the cache: it becomes 1
-    when a call met a position past its table or on no page of the cache."""
+    when a call met a position past its table or on no page of the cache.
+    Checked when it is made; its tensors are not exchanged afterwards."""
 
     k_codes: torch.Tensor  # int32 view of the uint32 words [n_pages, kv_heads, page_size, head_dim*bits/32]
     v_codes: torch.Tensor
@@ -515,81 +516,103 @@ class KVCache:
     bits: int
     info: torch.Tensor  # int32 [1] (device)
 
+    def __post_init__(self):
+        _kv_check_format(self.k_grid.shape, self.head_dim, self.bits)
+        rows = self.k_grid.shape
+        codes = (*rows, self.head_dim * self.bits // 32)
+        for name, shape in (("k_codes", codes), ("v_codes", codes), ("k_grid", rows), ("v_grid", rows), ("info", (1,))):
+            t = getattr(self, name)
+            _on_gpu(name, t)
+            if t.shape != shape or t.dtype != torch.int32 or not t.is_contiguous() or t.device != self.k_grid.device:
+                raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor on the cache's device")
+        struct = _KvCacheStruct(_ptr(self.k_codes), _ptr(self.v_codes), _ptr(self.k_grid), _ptr(self.v_grid), rows[0],
+                                rows[2], rows[1], self.head_dim, self.bits)
+        object.__setattr__(self, "_struct", struct)
+        object.__setattr__(self, "_ref", ctypes.byref(struct))
+        object.__setattr__(self, "_index", self.k_grid.get_device())
+        object.__setattr__(self, "_heads", rows[1])
+
+
+def _kv_check_format(rows, head_dim: int, bits: int) -> None:
+    if bits not in (4, 8):
+        raise ValueError("bits must be 4 or 8")
+    if not 16 <= head_dim <= 256 or head_dim % 16 != 0:
+        raise ValueError("head_dim must be a multiple of 16, 16 to 256")
+    if len(rows) != 3 or min(rows) < 1:
+        raise ValueError("the grids must be [n_pages, kv_heads, page_size], each at least 1")
+    if not 16 <= rows[2] <= 1024 or rows[2] & (rows[2] - 1):
+        raise ValueError("page_size must be a power of two, 16 to 1024")
+
 
 def gptq_kv_cache_alloc(n_pages: int, page_size: int, kv_heads: int, head_dim: int, bits: int, device) -> KVCache:
     """A zero-filled cache of n_pages pages of page_size tokens."""
-    if bits not in (4, 8):
-        raise ValueError("bits must be 4 or 8")
-    if head_dim % 16 != 0 or not 16 <= head_dim <= 256:
-        raise ValueError("head_dim must be a multiple of 16, 16 to 256")
-    if page_size & (page_size - 1) or not 16 <= page_size <= 1024:
-        raise ValueError("page_size must be a power of two, 16 to 1024")
-    if n_pages < 1 or kv_heads < 1:
-        raise ValueError("n_pages and kv_heads must be at least 1")
     rows = (n_pages, kv_heads, page_size)
+    _kv_check_format(rows, head_dim, bits)
     z = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)
     return KVCache(k_codes=z(*rows, head_dim * bits // 32), v_codes=z(*rows, head_dim * bits // 32), k_grid=z(*rows),
                    v_grid=z(*rows), head_dim=head_dim, bits=bits, info=z(1))
 
 
-def _kv_structs(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, starts: Optional[torch.Tensor],
-                n_tokens: int):
-    """The two structs of a call, after the checks of shapes and devices."""
-    dev = cache.k_codes.device
-    tensors = [("cache.k_codes", cache.k_codes), ("cache.v_codes", cache.v_codes), ("cache.k_grid", cache.k_grid),
-               ("cache.v_grid", cache.v_grid), ("cache.info", cache.info), ("table", table), ("lens", lens)]
-    if starts is not None:
-        tensors.append(("starts", starts))
-    for name, t in tensors:
-        _on_gpu(name, t)
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
-        if t.dtype != torch.int32:
-            raise ValueError(f"{name} must be int32")
-        if name != "table" and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    grid = cache.k_grid.shape
-    if len(grid) != 3 or cache.v_grid.shape != grid:
-        raise ValueError("cache grids must be [n_pages, kv_heads, page_size]")
-    codes = (*grid, cache.head_dim * cache.bits // 32)
-    if cache.k_codes.shape != codes or cache.v_codes.shape != codes:
-        raise ValueError("cache codes must be [n_pages, kv_heads, page_size, head_dim * bits / 32]")
-    if cache.info.numel() != 1:
-        raise ValueError("cache.info must hold one element")
-    if lens.dim() != 1:
-        raise ValueError("lens must be a vector")
+def _kv_ints(name: str, t: torch.Tensor, index: int) -> None:
+    # get_device() is -1 for a CPU tensor
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the cache's GPU")
+    if t.dtype != torch.int32:
+        raise ValueError(f"{name} must be int32")
+
+
+def _kv_batch(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, starts: Optional[torch.Tensor], n_tokens: int):
+    """The batch struct of a call, after the checks of shapes and devices."""
+    index = cache._index
+    _kv_ints("table", table, index)
+    _kv_ints("lens", lens, index)
+    if lens.dim() != 1 or not lens.is_contiguous():
+        raise ValueError("lens must be a contiguous vector")
     batch = lens.shape[0]
     if table.dim() != 2 or table.shape[0] != batch or (table.shape[1] > 1 and table.stride(1) != 1):
         raise ValueError("table must be [batch, max_pages] with unit column stride")
-    if starts is not None and starts.shape != (batch + 1,):
-        raise ValueError("starts must be [batch + 1]")
-    if starts is None and n_tokens != batch:
-        raise ValueError("without starts there is one token a sequence")
-    c = _KvCacheStruct(_ptr(cache.k_codes), _ptr(cache.v_codes), _ptr(cache.k_grid), _ptr(cache.v_grid), grid[0],
-                       grid[2], grid[1], cache.head_dim, cache.bits)
-    ld = table.stride(0) if batch > 1 else table.shape[1]
-    b = _KvBatchStruct(_ptr(table), ld, table.shape[1], _ptr(lens), _ptr(starts), batch, n_tokens)
-    return c, b
+    if starts is None:
+        if n_tokens != batch:
+            raise ValueError("without starts there is one token a sequence")
+        sp = None
+    else:
+        _kv_ints("starts", starts, index)
+        if starts.shape != (batch + 1,) or not starts.is_contiguous():
+            raise ValueError("starts must be a contiguous [batch + 1] vector")
+        sp = starts.data_ptr()
+    width = table.shape[1]
+    return _KvBatchStruct(table.data_ptr(), table.stride(0) if batch > 1 else width, width, lens.data_ptr(), sp, batch,
+                          n_tokens)
 
 
-def _kv_dtype(name: str, dtype: torch.dtype) -> int:
-    codes = {torch.float16: GPTQ_F16, torch.float32: GPTQ_F32, torch.bfloat16: GPTQ_BF16}
-    if dtype not in codes:
-        raise TypeError(f"{name}: unsupported dtype {dtype} (float16, bfloat16 or float32)")
-    return codes[dtype]
+_KV_DTYPES = {torch.float16: GPTQ_F16, torch.float32: GPTQ_F32, torch.bfloat16: GPTQ_BF16}
 
 
-def _kv_rows(name: str, t: torch.Tensor, n: Optional[int], heads: Optional[int], dim: int, dev) -> int:
-    """Checks [n_tokens, heads, dim] with heads and elements contiguous; returns the token stride."""
-    _on_gpu(name, t)
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
-    if (t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads)
-            or (n is not None and t.shape[0] != n)):
-        raise ValueError(f"{name} must be [n_tokens, heads, head_dim] of the call and its cache")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim):
+def _kv_dtype(name: str, t: torch.Tensor) -> int:
+    code = _KV_DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype} (float16, bfloat16 or float32)")
+    return code
+
+
+def _kv_rows(name: str, t: torch.Tensor, n: int, heads: int, dim: int, index: int) -> int:
+    """Checks [n, heads, dim] with heads and elements contiguous; returns the token stride."""
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the cache's GPU")
+    if t.shape != (n, heads, dim):
+        raise ValueError(f"{name} must be [n_tokens, heads, head_dim] = {[n, heads, dim]}, not {list(t.shape)}")
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != dim):
         raise ValueError(f"{name} must have its heads and their elements contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * dim
+    return st[0] if n > 1 else heads * dim
+
+
+def _kv_call(index: int, fn, *args) -> int:
+    """Calls fn(*args, stream) on device ``index`` and its current stream."""
+    if torch.cuda.current_device() == index:
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
 def gptq_kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -599,18 +622,17 @@ def gptq_kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table:
     ``lens`` [batch] counts each sequence's tokens with these, rows
     ``starts[b]:starts[b + 1]`` are sequence b's (None: one each), ``table``
     [batch, max_pages] holds its pages."""
-    dev = cache.k_codes.device
+    if k.dim() != 3:
+        raise ValueError("k must be [n_tokens, kv_heads, head_dim]")
     n = k.shape[0]
-    c, b = _kv_structs(cache, table, lens, starts, n)
-    heads = cache.k_grid.shape[1]
-    ldk, ldv = (_kv_rows(name, t, n, heads, cache.head_dim, dev) for name, t in (("k", k), ("v", v)))
+    b = _kv_batch(cache, table, lens, starts, n)
+    ldk = _kv_rows("k", k, n, cache._heads, cache.head_dim, cache._index)
+    ldv = _kv_rows("v", v, n, cache._heads, cache.head_dim, cache._index)
     if v.dtype != k.dtype:
         raise ValueError("k and v must have the same dtype")
-    lib = load()
-    with torch.cuda.device(dev):
-        _check("gptq_kv_cache_write",
-               lib.gptq_kv_cache_write(ctypes.byref(c), ctypes.byref(b), _ptr(k), _ptr(v), _kv_dtype("k", k.dtype), ldk,
-                                       ldv, _ptr(cache.info), _stream()))
+    status = _kv_call(cache._index, load().gptq_kv_cache_write, cache._ref, ctypes.byref(b), k.data_ptr(), v.data_ptr(),
+                      _kv_dtype("k", k), ldk, ldv, cache.info.data_ptr())
+    _check("gptq_kv_cache_write", status)
 
 
 def gptq_kv_cache_read(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, starts: Optional[torch.Tensor] = None,
@@ -620,27 +642,27 @@ def gptq_kv_cache_read(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, 
     ``n_tokens`` rows in all, needed with ``starts`` unless ``out`` = (k, v)
     is given). Rows past ``starts[batch]`` are left as they are (unspecified
     in new tensors)."""
-    dev = cache.k_codes.device
-    heads = cache.k_grid.shape[1]
     if out is None:
         if n_tokens is None:
             if starts is not None:
                 raise ValueError("n_tokens is needed with starts")
             n_tokens = lens.shape[0]
-        out = tuple(torch.empty((n_tokens, heads, cache.head_dim), dtype=dtype, device=dev) for _ in range(2))
-    k, v = out
-    n = k.shape[0]
-    if n_tokens is not None and n_tokens != n:
-        raise ValueError("out has another number of rows than n_tokens")
-    c, b = _kv_structs(cache, table, lens, starts, n)
-    ldk, ldv = (_kv_rows(name, t, n, heads, cache.head_dim, dev) for name, t in (("k", k), ("v", v)))
+        shape = (n_tokens, cache._heads, cache.head_dim)
+        k = torch.empty(shape, dtype=dtype, device=cache.info.device)
+        v = torch.empty(shape, dtype=dtype, device=cache.info.device)
+    else:
+        k, v = out
+        if k.dim() != 3 or (n_tokens is not None and n_tokens != k.shape[0]):
+            raise ValueError("out must be (k, v), each [n_tokens, kv_heads, head_dim]")
+        n_tokens = k.shape[0]
+    b = _kv_batch(cache, table, lens, starts, n_tokens)
+    ldk = _kv_rows("k", k, n_tokens, cache._heads, cache.head_dim, cache._index)
+    ldv = _kv_rows("v", v, n_tokens, cache._heads, cache.head_dim, cache._index)
     if v.dtype != k.dtype:
         raise ValueError("k and v must have the same dtype")
-    lib = load()
-    with torch.cuda.device(dev):
-        _check("gptq_kv_cache_read",
-               lib.gptq_kv_cache_read(ctypes.byref(c), ctypes.byref(b), _ptr(k), _ptr(v), _kv_dtype("out", k.dtype),
-                                      ldk, ldv, _ptr(cache.info), _stream()))
+    status = _kv_call(cache._index, load().gptq_kv_cache_read, cache._ref, ctypes.byref(b), k.data_ptr(), v.data_ptr(),
+                      _kv_dtype("out", k), ldk, ldv, cache.info.data_ptr())
+    _check("gptq_kv_cache_read", status)
     return k, v
 
 
@@ -649,17 +671,14 @@ def gptq_kv_attention_workspace_size(cache: KVCache, table: torch.Tensor, n_toke
     """Bytes of workspace that gptq_kv_attention takes for n_tokens rows of
     q_heads heads over the sequences of ``table`` (``ragged``: with starts;
     None: the larger of both where both are possible)."""
-    grid = cache.k_grid.shape
-    c = _KvCacheStruct(_ptr(cache.k_codes), _ptr(cache.v_codes), _ptr(cache.k_grid), _ptr(cache.v_grid), grid[0],
-                       grid[2], grid[1], cache.head_dim, cache.bits)
-    lib = load()
-    sizes = []
-    p = _ptr(table)
+    batch, width = table.shape
+    p = table.data_ptr()
+    sizes = [0]
     for r in (True, False) if ragged is None else (ragged,):
-        if r or n_tokens == table.shape[0]:
-            b = _KvBatchStruct(p, table.shape[1], table.shape[1], p, p if r else None, table.shape[0], n_tokens)
-            sizes.append(lib.gptq_kv_attention_workspace_size(ctypes.byref(c), ctypes.byref(b), q_heads))
-    return max(sizes, default=0)
+        if r or n_tokens == batch:
+            b = _KvBatchStruct(p, width, width, p, p if r else None, batch, n_tokens)
+            sizes.append(load().gptq_kv_attention_workspace_size(cache._ref, ctypes.byref(b), q_heads))
+    return max(sizes)
 
 
 def gptq_kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor,
@@ -672,31 +691,30 @@ def gptq_kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens
     default 1 / sqrt(head_dim); ``slopes`` fp32 [q_heads]: linear position
     biases. Rows past ``starts[batch]`` are left as they are (unspecified in
     a new tensor)."""
-    dev = cache.k_codes.device
-    n = q.shape[0]
-    c, b = _kv_structs(cache, table, lens, starts, n)
-    ldq = _kv_rows("q", q, n, None, cache.head_dim, dev)
-    hq = q.shape[1]
-    if hq % cache.k_grid.shape[1] != 0:
-        raise ValueError("q's heads must be a multiple of the cache's")
-    if slopes is not None:
-        _on_gpu("slopes", slopes)
-        if slopes.device != dev or slopes.dtype != torch.float32 or slopes.shape != (hq,) or not slopes.is_contiguous():
-            raise ValueError("slopes must be a contiguous float32 [q_heads] vector on the cache's device")
+    index = cache._index
+    if q.dim() != 3 or q.shape[1] < 1 or q.shape[1] % cache._heads != 0:
+        raise ValueError("q must be [n_tokens, q_heads, head_dim], its heads a multiple of the cache's")
+    n, hq = q.shape[0], q.shape[1]
+    b = _kv_batch(cache, table, lens, starts, n)
+    ldq = _kv_rows("q", q, n, hq, cache.head_dim, index)
+    if slopes is not None and (slopes.get_device() != index or slopes.dtype != torch.float32 or slopes.shape != (hq,)
+                               or not slopes.is_contiguous()):
+        raise ValueError("slopes must be a contiguous float32 [q_heads] vector on the cache's GPU")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype if dtype is None else dtype, device=dev)
+        out = torch.empty((n, hq, cache.head_dim), dtype=q.dtype if dtype is None else dtype, device=q.device)
     elif dtype is not None and out.dtype != dtype:
         raise ValueError("out has another dtype than asked for")
-    ldo = _kv_rows("out", out, n, hq, cache.head_dim, dev)
+    ldo = _kv_rows("out", out, n, hq, cache.head_dim, index)
     lib = load()
-    with torch.cuda.device(dev):
-        need = lib.gptq_kv_attention_workspace_size(ctypes.byref(c), ctypes.byref(b), hq)
-        if ws is not None and (ws.device != dev or not ws.is_contiguous()):
-            raise ValueError("ws must be contiguous and on the cache's device")
-        ws = _workspace(need, dev, ws)
-        _check("gptq_kv_attention",
-               lib.gptq_kv_attention(ctypes.byref(c), ctypes.byref(b), _ptr(q), _kv_dtype("q", q.dtype), hq, ldq,
-                                     cache.head_dim ** -0.5 if scale is None else float(scale), _ptr(slopes), _ptr(out),
-                                     _kv_dtype("out", out.dtype), ldo, _ptr(ws), ws.numel() * ws.element_size(),
-                                     _ptr(cache.info), _stream()))
+    bref = ctypes.byref(b)
+    need = lib.gptq_kv_attention_workspace_size(cache._ref, bref, hq)
+    if need and (ws is None or ws.nbytes < need):
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif ws is not None and (ws.get_device() != index or not ws.is_contiguous()):
+        raise ValueError("ws must be contiguous and on the cache's GPU")
+    status = _kv_call(index, lib.gptq_kv_attention, cache._ref, bref, q.data_ptr(), _kv_dtype("q", q), hq, ldq,
+                      cache.head_dim**-0.5 if scale is None else scale, None if slopes is None else slopes.data_ptr(),
+                      out.data_ptr(), _kv_dtype("out", out), ldo, ws.data_ptr() if need else None, need,
+                      cache.info.data_ptr())
+    _check("gptq_kv_attention", status)
     return out

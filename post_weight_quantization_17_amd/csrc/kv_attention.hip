@@ -69,6 +69,12 @@ struct AttArgs {
   int splits;
 };
 
+// Waves that share a SIMD: as many as the registers of a form leave without
+// spilling (a tile in flight and one in work, the sums of DP / 16 MFMAs).
+constexpr int att_waves_per_simd(int bits, int dp, bool split) {
+  return dp == 256 ? (bits == 8 && split ? 1 : 2) : dp == 128 ? (bits == 8 && split ? 2 : 3) : (split ? 3 : 4);
+}
+
 // The row blocks of a sequence with n new tokens.
 __host__ __device__ __forceinline__ int64_t row_blocks(int64_t n, int ratio) {
   return (n * ratio + ATT_ROWS - 1) / ATT_ROWS;
@@ -76,37 +82,39 @@ __host__ __device__ __forceinline__ int64_t row_blocks(int64_t n, int ratio) {
 
 // How the keys [0, kend) of a row block are split: chunk keys a workgroup,
 // `active` workgroups. Chunks are whole multiples of the 4 waves' tiles.
+// Lengths are int32, so key positions and their sums here fit 32 bits.
 struct Split {
-  int64_t chunk;
+  uint32_t chunk;
   int active;
 };
-__device__ __forceinline__ Split split_keys(int64_t kend, int splits) {
-  constexpr int64_t step = ATT_WAVES * ATT_TILE;
-  int64_t chunk = (kend + splits - 1) / splits;
+__device__ __forceinline__ Split split_keys(uint32_t kend, uint32_t splits) {
+  constexpr uint32_t step = ATT_WAVES * ATT_TILE;
+  uint32_t chunk = (kend + splits - 1) / splits;
   chunk = (chunk + step - 1) / step * step;
   if (chunk < ATT_MIN_CHUNK) chunk = ATT_MIN_CHUNK;
-  const int64_t n = (kend + chunk - 1) / chunk;
+  const uint32_t n = (kend + chunk - 1) / chunk;
   return Split{chunk, int(n < 1 ? 1 : n)};
 }
 
-// A sequence's share of the new tokens.
+// A sequence's share of the new tokens. The launch has fewer than 2^24
+// 16-row blocks, so n * ratio fits 32 bits.
 struct Seq {
-  int64_t b;   // sequence, -1: none
-  int64_t t0;  // its first token
-  int64_t n;   // its new tokens
-  int64_t rb;  // row block within it
+  int b;   // sequence, -1: none
+  int t0;  // its first token
+  int n;   // its new tokens
+  int rb;  // row block within it
 };
 
 // The sequence and row block that workgroup number `at` works on. Uniform
 // over the wave, all of whose lanes take part.
-__device__ __forceinline__ Seq find_block(const KvBatch& q, int ratio, int64_t at, int lane) {
+__device__ __forceinline__ Seq find_block(const KvBatch& q, int ratio, int at, int lane) {
   if (!q.starts) {
-    const int64_t per = row_blocks(1, ratio);
+    const int per = int(row_blocks(1, ratio));
     return Seq{at / per, at / per, 1, at % per};
   }
   int64_t before = 0;  // row blocks of the sequences passed
-  for (int64_t b0 = 0; b0 < q.batch; b0 += 64) {
-    const int64_t b = b0 + lane;
+  for (int b0 = 0; b0 < q.batch; b0 += 64) {
+    const int b = b0 + lane;
     int64_t t0 = 0, n = 0;
     if (b < q.batch) {
       t0 = q.starts[b];
@@ -123,22 +131,23 @@ __device__ __forceinline__ Seq find_block(const KvBatch& q, int ratio, int64_t a
     const uint64_t past = __ballot(before + sum > at);
     if (past != 0) {
       const int src = __ffsll((unsigned long long)past) - 1;
-      const int64_t first = before + __shfl(sum - mine, src);
-      return Seq{b0 + src, __shfl(t0, src), __shfl(n, src), at - first};
+      const int first = int(before + __shfl(sum - mine, src));
+      return Seq{__builtin_amdgcn_readfirstlane(b0 + src), __builtin_amdgcn_readfirstlane(__shfl(int(t0), src)),
+                 __builtin_amdgcn_readfirstlane(__shfl(int(n), src)), __builtin_amdgcn_readfirstlane(at - first)};
     }
     before += __shfl(sum, 63);
   }
   return Seq{-1, 0, 0, 0};
 }
 
-// Keys that row block rb of a sequence of `len` cached tokens, n of them
-// new, can see: those of its last row.
-__device__ __forceinline__ int64_t keys_seen(int64_t len, int64_t n, int64_t i, int64_t cap) {
+// Keys that new token i of n of a sequence of `len` tokens sees, `cap` of
+// which the table reaches.
+__device__ __forceinline__ uint32_t keys_seen(int64_t len, int n, int i, int64_t cap) {
   const int64_t end = len - n + i + 1;
-  return end < 0 ? 0 : end > cap ? cap : end;
+  return uint32_t(end < 0 ? 0 : end > cap ? cap : end);
 }
-__device__ __forceinline__ int64_t block_last_row(int64_t n, int ratio, int64_t rb) {
-  const int64_t last = rb * ATT_ROWS + ATT_ROWS - 1, rows = n * ratio;
+__device__ __forceinline__ int block_last_row(int n, int ratio, int rb) {
+  const int last = rb * ATT_ROWS + ATT_ROWS - 1, rows = n * ratio;
   return last < rows ? last : rows - 1;
 }
 
@@ -163,16 +172,35 @@ __device__ __forceinline__ half8 as_half8(uint32_t a, uint32_t b, uint32_t c, ui
 // position of the code in it.
 template <int BITS>
 struct Half {
-  static constexpr float off = BITS == 4 ? 16.0f : 1024.0f;
-  static constexpr uint32_t magic = BITS == 4 ? 0x4C004C00u : 0x64006400u;
-  static constexpr int at = BITS == 4 ? 6 : 0;
+  static constexpr float off = BITS == 4 ? 64.0f : 1024.0f;
+  static constexpr uint32_t magic = BITS == 4 ? 0x54005400u : 0x64006400u;
+  static constexpr int at = BITS == 4 ? 4 : 0;
 };
 
-// 4-bit codes: code i (0..3) of each 16-bit half of w, as two halves 16 + c.
+// The conversion's constants, kept in registers: a mask in an SGPR and the
+// exponent pattern in a VGPR make mask-and-merge one v_and_or_b32, which
+// takes no literals.
+struct Consts {
+  uint32_t mask, magic;
+};
+template <int BITS>
+__device__ __forceinline__ Consts conversion_consts() {
+  Consts k{0x00F000F0u, Half<BITS>::magic};
+  KV_OPAQUE_S(k.mask);
+  KV_OPAQUE_V(k.magic);
+  return k;
+}
+
+// 4-bit codes: code i (0..3) of each 16-bit half of w, as two halves 64 + c.
 template <int I>
-__device__ __forceinline__ uint32_t nibbles(uint32_t w) {
-  constexpr int up = 6 - 4 * I;
-  return ((up > 0 ? w << up : w >> -up) & 0x03C003C0u) | Half<4>::magic;
+__device__ __forceinline__ uint32_t nibbles(uint32_t w, const Consts& k) {
+  constexpr int up = 4 - 4 * I;
+  return ((up > 0 ? w << up : w >> -up) & k.mask) | k.magic;
+}
+// 8-bit codes: bytes A and B of w, as two halves 1024 + c.
+template <int A, int B>
+__device__ __forceinline__ uint32_t byte_pair(uint32_t w, const Consts& k) {
+  return __builtin_amdgcn_perm(k.magic, w, 0x05000500u | A | B << 16);
 }
 
 // The 8 codes of a lane's k-slots in one MFMA of the first product. 4 bits:
@@ -182,17 +210,17 @@ struct KeyOrder {
   static constexpr int code(int i) { return BITS == 4 ? (i % 2) * 4 + i / 2 : i; }
 };
 template <int BITS>
-__device__ __forceinline__ void key_codes(const uint32_t* w, uint32_t (&h)[4]) {
+__device__ __forceinline__ void key_codes(const uint32_t* w, uint32_t (&h)[4], const Consts& k) {
   if constexpr (BITS == 4) {
-    h[0] = nibbles<0>(w[0]);
-    h[1] = nibbles<1>(w[0]);
-    h[2] = nibbles<2>(w[0]);
-    h[3] = nibbles<3>(w[0]);
+    h[0] = nibbles<0>(w[0], k);
+    h[1] = nibbles<1>(w[0], k);
+    h[2] = nibbles<2>(w[0], k);
+    h[3] = nibbles<3>(w[0], k);
   } else {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      h[2 * i] = __builtin_amdgcn_perm(0x64646464u, w[i], 0x04010400u);
-      h[2 * i + 1] = __builtin_amdgcn_perm(0x64646464u, w[i], 0x04030402u);
+      h[2 * i] = byte_pair<0, 1>(w[i], k);
+      h[2 * i + 1] = byte_pair<2, 3>(w[i], k);
     }
   }
 }
@@ -207,11 +235,32 @@ struct Tile {
   uint32_t v[8][VW];
   uint4 kg[2], vg[2];
   uint32_t kz[2];
-  uint32_t ok;  // bit t: subtile t lies on a page
 };
 
+// N words at p, which is aligned to the largest power of two that divides
+// their size, 16 bytes at most.
+template <int N>
+__device__ __forceinline__ void load_words(const char* p, uint32_t* w) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const uint2 v = reinterpret_cast<const uint2*>(p)[i];
+      w[2 * i] = v.x, w[2 * i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+  }
+}
+
 template <int BITS, int DP, bool FULL, bool SPLIT>
-__global__ void __launch_bounds__(64 * ATT_WAVES)
+__global__ void __launch_bounds__(64 * ATT_WAVES, att_waves_per_simd(BITS, DP, SPLIT))
 kv_attend(AttArgs a) {
   using TL = Tile<BITS, DP>;
   constexpr int NJ = DP / 32, KW = TL::KW, DPL = TL::DPL, VW = TL::VW;
@@ -224,32 +273,119 @@ kv_attend(AttArgs a) {
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int g = lane / 16, n16 = lane % 16;
   const int kv = int(blockIdx.x % unsigned(c.heads));
-  const Seq sq = find_block(a.b, a.ratio, int64_t(blockIdx.x / unsigned(c.heads)), lane);
+  const Seq sq = find_block(a.b, a.ratio, int(blockIdx.x / unsigned(c.heads)), lane);
   if (sq.b < 0 || sq.b >= a.b.batch) return;  // whole workgroup; uniform
 
   const int64_t cap = a.b.max_pages << c.shift;
-  const int64_t len = a.b.lens[sq.b];
-  const int64_t last_row = block_last_row(sq.n, a.ratio, sq.rb);
-  const int nrows = int(last_row - sq.rb * ATT_ROWS) + 1;
-  const int64_t kend = keys_seen(len, sq.n, last_row / a.ratio, cap);
+  const int64_t len = __builtin_amdgcn_readfirstlane(a.b.lens[sq.b]);
+  const int last_row = block_last_row(sq.n, a.ratio, sq.rb);
+  const int nrows = last_row - sq.rb * ATT_ROWS + 1;
+  const uint32_t kend = keys_seen(len, sq.n, last_row / a.ratio, cap);
   if (len > cap && threadIdx.x == 0) kv_flag(a.info);
   const Split sp = split_keys(kend, a.splits);
   if (int(blockIdx.y) >= sp.active) return;
-  const int64_t k0 = int64_t(blockIdx.y) * sp.chunk;
-  const int64_t k1 = kend < k0 + sp.chunk ? kend : k0 + sp.chunk;
+  const uint32_t k0 = blockIdx.y * sp.chunk;
+  const uint32_t k1 = kend - k0 < sp.chunk ? kend : k0 + sp.chunk;
 
   // This lane's query row, and the keys that every row of the block sees.
-  const int64_t row = sq.rb * ATT_ROWS + n16;
+  const int row = sq.rb * ATT_ROWS + n16;
   const bool live = n16 < nrows;
-  const int64_t i = live ? row / a.ratio : 0;
-  const int hq = kv * a.ratio + (live ? int(row % a.ratio) : 0);
-  const int64_t lim = live ? keys_seen(len, sq.n, i, cap) : 0;
-  const int64_t all_see = keys_seen(len, sq.n, sq.rb * ATT_ROWS / a.ratio, cap);
-  const int64_t pos = len - sq.n + i;
+  const int i = live ? row / a.ratio : 0;
+  const int hq = kv * a.ratio + (live ? row - i * a.ratio : 0);
+  const uint32_t lim = live ? keys_seen(len, sq.n, i, cap) : 0;
+  const uint32_t all_see = keys_seen(len, sq.n, sq.rb * ATT_ROWS / a.ratio, cap);
+  const int pos = int(len - sq.n + i);
   const float slope = a.slopes ? a.slopes[hq] * LOG2E : 0.0f;
 
+  // The tiles of this wave. A tile's pages are looked up a tile ahead, its
+  // keys are loaded while the tile before is in its softmax and second
+  // product, its values while it is in its own first product: the registers
+  // of one tile suffice, and loads are always in flight.
+  constexpr uint32_t step = ATT_WAVES * ATT_TILE;
+  const int words = FULL ? DP * BITS / 32 : c.words;
+  const int32_t* const pages = a.b.table + sq.b * a.b.ld;
+  struct Ids {
+    int id[2];
+  };
+  const auto look_up = [&](uint32_t p0) {
+    Ids r{{-1, -1}};
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (p0 + 16 * u < k1) r.id[u] = pages[(p0 + 16 * u) >> c.shift];
+    return r;
+  };
+  // Cache row of each 16-key subtile's first key, and which subtiles (bit u)
+  // lie on a page. The others read the first page's rows and are masked.
+  struct Rows {
+    int64_t at[2];
+    uint32_t ok;
+  };
+  const auto locate = [&](uint32_t p0, const Ids& ids) {
+    Rows r;
+    r.ok = 0;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t p = p0 + 16 * u;
+      int64_t id = __builtin_amdgcn_readfirstlane(ids.id[u]);
+      if (id >= 0 && id < c.n_pages) {
+        r.ok |= 1u << u;
+      } else {
+        if (p < k1) kv_flag(a.info);
+        id = 0;
+      }
+      r.at[u] = ((id * c.heads + kv) << c.shift) + (p & ((1u << c.shift) - 1));
+    }
+    return r;
+  };
+  const int vc = n16 * DPL < c.dim ? n16 : 0;  // lanes past the head's end repeat the first one's codes
+  const uint32_t k_off = FULL ? 4u * (n16 * words + g * KW) : 4u * n16 * words;
+  const uint32_t v_off = DPL * BITS == 16 ? 16u * g * words + 2u * vc : 16u * g * words + 4u * VW * vc;
+  const auto blk = [&](int j) { return FULL ? g * NJ + j : 4 * j + g; };  // blocks of 8 d of this lane
+  TL t;
+  const auto load_keys = [&](const Rows& at) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const char* kr = reinterpret_cast<const char*>(c.k_codes + at.at[u] * words);
+      const char* gr = reinterpret_cast<const char*>(c.k_grid + at.at[u]);
+      if constexpr (FULL) {
+        load_words<KW>(kr + k_off, t.k[u]);
+      } else {
+        constexpr int W = BITS / 4;  // words of a block
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          load_words<W>(kr + (k_off + 4u * W * (8 * blk(j) < c.dim ? blk(j) : 0)), &t.k[u][W * j]);
+      }
+      t.kg[u] = *reinterpret_cast<const uint4*>(gr + 16u * g);
+      if constexpr (SPLIT) t.kz[u] = *reinterpret_cast<const uint32_t*>(gr + 4u * n16);
+    }
+  };
+  const auto load_values = [&](const Rows& at) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      t.vg[u] = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(c.v_grid + at.at[u]) + 16u * g);
+      const char* vr = reinterpret_cast<const char*>(c.v_codes + at.at[u] * words);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const char* vp = vr + 4 * r * words + v_off;
+        if constexpr (DPL * BITS == 16)
+          t.v[4 * u + r][0] = *reinterpret_cast<const uint16_t*>(vp);
+        else
+          load_words<VW>(vp, t.v[4 * u + r]);
+      }
+    }
+  };
+
+  uint32_t p0 = k0 + wave * ATT_TILE;
+  Rows at = {};
+  Ids ids = look_up(p0);
+  if (p0 < k1) {
+    at = locate(p0, ids);
+    load_keys(at);
+    load_values(at);
+    ids = look_up(p0 + step);
+  }
+
   // Queries: block j of 8 elements of this lane, in the order of the codes.
-  const auto blk = [&](int j) { return FULL ? g * NJ + j : 4 * j + g; };
   half8 qh[NJ], ql[NJ];
   float qsum = 0.0f, row_scale;
   {
@@ -261,7 +397,7 @@ kv_attend(AttArgs a) {
       for (int e = 0; e < 8; ++e) f[j][e] = 0.0f;
       const int d0 = 8 * blk(j);
       if (live && d0 < c.dim) {
-        const int64_t at = (sq.t0 + i) * a.ldq + int64_t(hq) * c.dim + d0;
+        const int64_t at = int64_t(sq.t0 + i) * a.ldq + int64_t(hq) * c.dim + d0;
         if (a.q_dtype == GPTQ_F16)
           load8(static_cast<const _Float16*>(a.q) + at, a.q_vec, f[j]);
         else if (a.q_dtype == GPTQ_BF16)
@@ -294,47 +430,11 @@ kv_attend(AttArgs a) {
 #pragma unroll
   for (int m = 0; m < DPL; ++m) o[m] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
   float M = ATT_LOWEST, l = 0.0f;
-  const int vc = n16 * DPL < c.dim ? n16 : 0;  // lanes past the head's end repeat the first one's codes
+  const Consts kc = conversion_consts<BITS>();
 
-  const auto load = [&](int64_t p0, TL& t) {
-    t.ok = 0;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t p = p0 + 16 * u;
-      int64_t id = -1;
-      if (p < k1) id = kv_page(c, a.b, sq.b, p, a.info);
-      if (id >= 0) t.ok |= 1u << u;
-      // Keys on no page read the first page's rows, which are masked.
-      const int64_t base = id < 0 ? int64_t(kv) << c.shift
-                                  : ((id * c.heads + kv) << c.shift) + (p & ((int64_t(1) << c.shift) - 1));
-      const uint32_t* kr = c.k_codes + base * c.words + n16 * c.words;
-      if constexpr (FULL) {
-#pragma unroll
-        for (int w = 0; w < KW; ++w) t.k[u][w] = kr[g * KW + w];
-      } else {
-        constexpr int W = BITS / 4;  // words of a block
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int w = 0; w < W; ++w) t.k[u][W * j + w] = 8 * blk(j) < c.dim ? kr[W * blk(j) + w] : 0u;
-      }
-      t.kg[u] = *reinterpret_cast<const uint4*>(c.k_grid + base + 4 * g);
-      t.vg[u] = *reinterpret_cast<const uint4*>(c.v_grid + base + 4 * g);
-      if constexpr (SPLIT) t.kz[u] = c.k_grid[base + n16];
-      const uint32_t* vr = c.v_codes + base * c.words + 4 * g * c.words;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if constexpr (DPL * BITS == 16) {
-          t.v[4 * u + r][0] = reinterpret_cast<const uint16_t*>(vr + r * c.words)[vc];
-        } else {
-#pragma unroll
-          for (int w = 0; w < VW; ++w) t.v[4 * u + r][w] = vr[r * c.words + VW * vc + w];
-        }
-      }
-    }
-  };
-
-  const auto compute = [&](int64_t p0, const TL& t) {
+  while (p0 < k1) {
+    const uint32_t ok = at.ok;
+    const bool more = p0 + step < k1;
     float x[8], sv[8];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -342,15 +442,15 @@ kv_attend(AttArgs a) {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         uint32_t h[4];
-        key_codes<BITS>(&t.k[u][j * (BITS / 4)], h);
+        key_codes<BITS>(&t.k[u][j * (BITS / 4)], h, kc);
         if constexpr (SPLIT) {
           const uint32_t z1 = MAGIC + (kv_zero<BITS>(t.kz[u]) * 0x10001u << Half<BITS>::at);
 #pragma unroll
           for (int e = 0; e < 4; ++e) h[e] = as_u32(as_half2(h[e]) - as_half2(z1));
         }
-        const half8 kc = as_half8(h[0], h[1], h[2], h[3]);
-        if constexpr (SPLIT) acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kc, ql[j], acc, 0, 0, 0);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kc, qh[j], acc, 0, 0, 0);
+        const half8 keys = as_half8(h[0], h[1], h[2], h[3]);
+        if constexpr (SPLIT) acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(keys, ql[j], acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(keys, qh[j], acc, 0, 0, 0);
       }
       const uint32_t kg[4] = {t.kg[u].x, t.kg[u].y, t.kg[u].z, t.kg[u].w};
       const uint32_t vg[4] = {t.vg[u].x, t.vg[u].y, t.vg[u].z, t.vg[u].w};
@@ -361,16 +461,21 @@ kv_attend(AttArgs a) {
         sv[4 * u + r] = kv_scale(vg[r]);
       }
     }
+    if (more) {
+      at = locate(p0 + step, ids);
+      load_keys(at);
+      ids = look_up(p0 + 2 * step);
+    }
     if (a.slopes) {
-      const float rel = float(int(p0 + 4 * g - pos));
+      const float rel = float(int(p0) + 4 * g - pos);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = fmaf(slope, rel + float(16 * (e / 4) + e % 4), x[e]);
     }
-    if (p0 + ATT_TILE > all_see || t.ok != 3u) {
-      const int64_t left = lim - p0 - 4 * g;
+    if (p0 + ATT_TILE > all_see || ok != 3u) {
+      const int left = int(lim) - int(p0) - 4 * g;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const bool seen = 16 * (e / 4) + e % 4 < left && (t.ok >> (e / 4) & 1u) != 0;
+        const bool seen = 16 * (e / 4) + e % 4 < left && (ok >> (e / 4) & 1u) != 0;
         x[e] = seen ? x[e] : -INFINITY;
         sv[e] = seen ? sv[e] : 0.0f;
       }
@@ -435,60 +540,48 @@ kv_attend(AttArgs a) {
       uint32_t h[4];
       if constexpr (BITS == 4) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = nibbles<0>(lo[e]);
+        for (int e = 0; e < 4; ++e) h[e] = nibbles<0>(lo[e], kc);
         product(8 * vw + 0, h);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = nibbles<1>(lo[e]);
+        for (int e = 0; e < 4; ++e) h[e] = nibbles<1>(lo[e], kc);
         product(8 * vw + 1, h);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = nibbles<2>(lo[e]);
+        for (int e = 0; e < 4; ++e) h[e] = nibbles<2>(lo[e], kc);
         product(8 * vw + 2, h);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = nibbles<3>(lo[e]);
+        for (int e = 0; e < 4; ++e) h[e] = nibbles<3>(lo[e], kc);
         product(8 * vw + 3, h);
         if constexpr (DPL > 4) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = nibbles<0>(hi[e]);
+          for (int e = 0; e < 4; ++e) h[e] = nibbles<0>(hi[e], kc);
           product(8 * vw + 4, h);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = nibbles<1>(hi[e]);
+          for (int e = 0; e < 4; ++e) h[e] = nibbles<1>(hi[e], kc);
           product(8 * vw + 5, h);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = nibbles<2>(hi[e]);
+          for (int e = 0; e < 4; ++e) h[e] = nibbles<2>(hi[e], kc);
           product(8 * vw + 6, h);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = nibbles<3>(hi[e]);
+          for (int e = 0; e < 4; ++e) h[e] = nibbles<3>(hi[e], kc);
           product(8 * vw + 7, h);
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = __builtin_amdgcn_perm(0x64646464u, lo[e], 0x04020400u);
+        for (int e = 0; e < 4; ++e) h[e] = byte_pair<0, 2>(lo[e], kc);
         product(4 * vw + 0, h);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = __builtin_amdgcn_perm(0x64646464u, lo[e], 0x04030401u);
+        for (int e = 0; e < 4; ++e) h[e] = byte_pair<1, 3>(lo[e], kc);
         product(4 * vw + 1, h);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = __builtin_amdgcn_perm(0x64646464u, hi[e], 0x04020400u);
+        for (int e = 0; e < 4; ++e) h[e] = byte_pair<0, 2>(hi[e], kc);
         product(4 * vw + 2, h);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = __builtin_amdgcn_perm(0x64646464u, hi[e], 0x04030401u);
+        for (int e = 0; e < 4; ++e) h[e] = byte_pair<1, 3>(hi[e], kc);
         product(4 * vw + 3, h);
       }
     }
-  };
-
-  // The next tile's loads are in flight while a tile is computed.
-  const int64_t step = ATT_WAVES * ATT_TILE;
-  int64_t p0 = k0 + wave * ATT_TILE;
-  if (p0 < k1) {
-    TL cur;
-    load(p0, cur);
-    for (; p0 < k1; p0 += step) {
-      TL next;
-      if (p0 + step < k1) load(p0 + step, next);
-      compute(p0, cur);
-      cur = next;
-    }
+    if (more) load_values(at);
+    p0 += step;
   }
 
   // Join the waves: waves 0 and 1 leave their sums, waves 2 and 3 add theirs.
@@ -521,9 +614,9 @@ kv_attend(AttArgs a) {
     __syncthreads();
   }
   for (int r = wave; r < nrows; r += ATT_WAVES) {
-    const int64_t at = sq.rb * ATT_ROWS + r;
+    const int at = sq.rb * ATT_ROWS + r;
     const int64_t t = sq.t0 + at / a.ratio;
-    const int h = kv * a.ratio + int(at % a.ratio);
+    const int h = kv * a.ratio + at % a.ratio;
     float top = lds_m[0][r];
     for (int w = 1; w < ATT_WAVES; ++w) top = fmaxf(top, lds_m[w][r]);
     float sum = 0.0f;
@@ -550,18 +643,21 @@ kv_attend(AttArgs a) {
   }
 }
 
-// Joins the splits of one row (token, query head), in their order: each wave
-// adds every fourth one, and the waves' sums are added in order.
+// Joins the splits of one row (token, query head). Every thread holds 4 of
+// the row's d for one residue of the splits (lanes of a power of two cover
+// the row), so a row's splits are read 4 to 64 at a time; the sums of the
+// residues are added in order.
 __global__ void __launch_bounds__(64 * ATT_WAVES)
 kv_join(AttArgs a) {
-  __shared__ float sums[ATT_WAVES][256];
+  __shared__ float weight[ATT_MAX_SPLITS];
+  __shared__ float4 sums[64 * ATT_WAVES];
   const KvCache& c = a.c;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const int64_t heads_q = int64_t(c.heads) * a.ratio;
   const int64_t t = int64_t(blockIdx.x) / heads_q;
   const int h = int(int64_t(blockIdx.x) % heads_q);
   // The token's sequence, and the keys of its row block as kv_attend took them.
-  int64_t b = t, t0 = t, n = 1;
+  int64_t b = t, t0 = t, n = 1;  // as in find_block
   if (a.b.starts) {
     int64_t cnt = 0;
     for (int64_t i0 = 0; i0 <= a.b.batch; i0 += 64) {
@@ -577,34 +673,51 @@ kv_join(AttArgs a) {
     if (n < 0 || t0 < 0 || t0 + n > a.b.n_tokens || t < t0 || t >= t0 + n) return;
   }
   const int64_t cap = a.b.max_pages << c.shift;
-  const int64_t rb = ((t - t0) * a.ratio + h % a.ratio) / ATT_ROWS;
-  const int64_t kend = keys_seen(a.b.lens[b], n, block_last_row(n, a.ratio, rb) / a.ratio, cap);
+  const int rb = (int(t - t0) * a.ratio + h % a.ratio) / ATT_ROWS;
+  const uint32_t kend = keys_seen(a.b.lens[b], int(n), block_last_row(int(n), a.ratio, rb) / a.ratio, cap);
   const Split sp = split_keys(kend, a.splits);
   if (sp.active <= 1) return;  // kv_attend wrote the row
 
   const int64_t stride = a.b.n_tokens * heads_q, pr = t * heads_q + h;
+  // Each wave works out the weights of all splits, 64 at a time.
   float top = ATT_LOWEST;
-  for (int s = 0; s < sp.active; ++s) top = fmaxf(top, a.part_ml[s * stride + pr].x);
-  float sum = 0.0f, o[4] = {};
-  for (int s = 0; s < sp.active; ++s) {
+  for (int s = lane; s < sp.active; s += 64) top = fmaxf(top, a.part_ml[s * stride + pr].x);
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) top = fmaxf(top, __shfl_xor(top, m));
+  float sum = 0.0f;
+  for (int s = lane; s < sp.active; s += 64) {
     const float2 ml = a.part_ml[s * stride + pr];
     const float f = __builtin_amdgcn_exp2f(ml.x - top);
+    if (wave == 0) weight[s] = f;
     sum += ml.y * f;
-    if (s % ATT_WAVES == wave) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int d = lane + 64 * e;
-        if (d < c.dim) o[e] = fmaf(a.part_o[(s * stride + pr) * c.dim + d], f, o[e]);
-      }
-    }
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) sums[wave][lane + 64 * e] = o[e];
+  for (int m = 1; m < 64; m *= 2) sum += __shfl_xor(sum, m);
   __syncthreads();
-  const int d = threadIdx.x;
+  const int quads = c.dim / 4;
+  const int per = quads <= 4 ? 4 : quads <= 8 ? 8 : quads <= 16 ? 16 : quads <= 32 ? 32 : 64;
+  const int d4 = int(threadIdx.x) % per, residue = int(threadIdx.x) / per, residues = 64 * ATT_WAVES / per;
+  float4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (d4 < quads) {
+    const float4* src = reinterpret_cast<const float4*>(a.part_o) + pr * quads + d4;
+#pragma unroll 4
+    for (int s = residue; s < sp.active; s += residues) {
+      const float4 v = src[s * stride * quads];
+      const float f = weight[s];
+      o.x = fmaf(v.x, f, o.x);
+      o.y = fmaf(v.y, f, o.y);
+      o.z = fmaf(v.z, f, o.z);
+      o.w = fmaf(v.w, f, o.w);
+    }
+  }
+  sums[threadIdx.x] = o;
+  __syncthreads();
+  const int d = int(threadIdx.x);
   if (d >= c.dim) return;
-  float v = sums[0][d];
-  for (int w = 1; w < ATT_WAVES; ++w) v += sums[w][d];
+  const float* flat = reinterpret_cast<const float*>(sums);
+  const int used = sp.active < residues ? sp.active : residues;
+  float v = 0.0f;
+  for (int r = 0; r < used; ++r) v += flat[r * per * 4 + d];
   v *= sum == 0.0f ? 0.0f : 1.0f / sum;
   const int64_t oo = t * a.ldo + int64_t(h) * c.dim + d;
   if (a.out_dtype == GPTQ_F16)
@@ -702,8 +815,8 @@ extern "C" int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch
   if (a.splits > 1) {
     if (ws_bytes < gptq_kv_attention_workspace_size(cache, batch, q_heads)) return GPTQ_E_WORKSPACE;
     if (!ws || reinterpret_cast<uintptr_t>(ws) % 16 != 0) return GPTQ_E_INVALID_ARG;
-    a.part_ml = static_cast<float2*>(ws);
-    a.part_o = reinterpret_cast<float*>(a.part_ml + int64_t(a.splits) * a.b.n_tokens * q_heads);
+    a.part_o = static_cast<float*>(ws);  // its rows stay 16-byte aligned: head_dim is a multiple of 16
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + int64_t(a.splits) * a.b.n_tokens * q_heads * a.c.dim);
   }
   const bool split = q_dtype == GPTQ_F32 || out_dtype == GPTQ_F32;
   const dim3 grid(unsigned(blocks), unsigned(a.splits));

@@ -7,6 +7,13 @@
 
 namespace gptq {
 
+// Keeps the compiler from seeing a constant, so that it stays in an SGPR or
+// a VGPR instead of becoming a literal of every instruction that uses it.
+#ifndef KV_OPAQUE_S
+#define KV_OPAQUE_S(x) asm("" : "+s"(x))
+#define KV_OPAQUE_V(x) asm("" : "+v"(x))
+#endif
+
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 
 // What the kernels need of gptq_kv_cache and gptq_kv_batch. `shift` is log2

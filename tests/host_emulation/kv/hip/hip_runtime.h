@@ -28,6 +28,8 @@
 #define __forceinline__ inline
 #define __launch_bounds__(...)
 #define __shared__ static
+#define KV_OPAQUE_S(x) ((void)(x))
+#define KV_OPAQUE_V(x) ((void)(x))
 
 struct dim3 {
   uint32_t x, y, z;
@@ -41,6 +43,9 @@ struct alignas(8) uint2 {
 };
 struct alignas(8) float2 {
   float x, y;
+};
+struct alignas(16) float4 {
+  float x, y, z, w;
 };
 
 typedef enum hipError_t { hipSuccess = 0 } hipError_t;
