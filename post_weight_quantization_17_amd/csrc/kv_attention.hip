@@ -46,8 +46,7 @@ constexpr int ATT_WAVES = 4;
 constexpr int ATT_ROWS = 16;                     // query rows of a workgroup
 constexpr int ATT_TILE = 32;                     // keys a wave takes at a time
 constexpr int ATT_MIN_CHUNK = 256;               // fewest keys of a workgroup when a row's keys are split
-constexpr int ATT_MAX_SPLITS = 128;
-constexpr int ATT_TARGET_GROUPS = 1024;          // workgroups that fill 256 CUs
+constexpr int ATT_MAX_TARGET = 4 * 256;          // most workgroups that the keys are split for (Seq)
 constexpr float ATT_W_TOP = 8.0f;                // log2 of the largest weight after a rescaling
 constexpr float ATT_W_LIMIT = 32768.0f;          // a weight above this asks for the next one
 constexpr float ATT_LOWEST = -3.402823466e38f;   // M before the first key
@@ -59,14 +58,17 @@ struct AttArgs {
   const void* q;
   void* out;
   const float* slopes;
-  float* part_o;   // [splits][n_tokens][q_heads][dim]
-  float2* part_ml; // [splits][n_tokens][q_heads]
+  float* part_o;    // [units][kv_heads][rows][dim]: a unit's partial sums
+  float2* part_ml;  // [units][kv_heads][rows]: their reference and weight sum
   int32_t* info;
   int64_t ldq, ldo;
   float scale;  // of the scores, in log2 units
   int ratio;    // query heads that share a key-value head
   int q_dtype, out_dtype, q_vec;
-  int splits;
+  int rows;     // rows of a unit in the workspace
+  int splits;   // 0: no row block's keys are split
+  int units;    // of the launch
+  int target;   // workgroups that the keys are split for
 };
 
 // Waves that share a SIMD: as many as the registers of a form leave without
@@ -75,69 +77,143 @@ constexpr int att_waves_per_simd(int bits, int dp, bool split) {
   return dp == 256 ? (bits == 8 && split ? 1 : 2) : dp == 128 ? (bits == 8 && split ? 2 : 3) : (split ? 3 : 4);
 }
 
+constexpr int att_buffers(int bits, int dp, bool split) { return 1; }
+
+__device__ __forceinline__ void store_out(const AttArgs& a, int64_t at, float v) {
+  if (a.out_dtype == GPTQ_F16)
+    static_cast<_Float16*>(a.out)[at] = from_f32<_Float16>(v);
+  else if (a.out_dtype == GPTQ_BF16)
+    static_cast<bf16*>(a.out)[at] = from_f32<bf16>(v);
+  else
+    static_cast<float*>(a.out)[at] = v;
+}
+
 // The row blocks of a sequence with n new tokens.
 __host__ __device__ __forceinline__ int64_t row_blocks(int64_t n, int ratio) {
   return (n * ratio + ATT_ROWS - 1) / ATT_ROWS;
 }
 
-// How the keys [0, kend) of a row block are split: chunk keys a workgroup,
-// `active` workgroups. Chunks are whole multiples of the 4 waves' tiles.
-// Lengths are int32, so key positions and their sums here fit 32 bits.
-struct Split {
+// A call's work is cut into units: one row block (of one key-value head) over
+// one chunk of its sequence's keys. The chunk is the same for all sequences,
+// so that units take about the same time however ragged the batch is: the
+// keys of all row blocks over the workgroups that the GPU is to be filled
+// with, in whole tiles of the 4 waves. Lengths are device data, so every
+// workgroup works the chunk out for itself, from the same numbers in the same
+// order. A sequence has ceil(len / chunk) units a row block (at least one,
+// which writes the zeros of rows without keys); those past a causal row
+// block's last key have nothing to do.
+//
+// The host's bound of the units (call_units) holds because each sequence has
+// at most len / chunk + 1 a row block, and chunk is at least the mean share.
+// The launch has fewer than 2^24 row blocks, so n * ratio fits 32 bits;
+// lengths are int32, so positions and their sums here do, too.
+struct Seq {
+  int b;       // sequence, -1: none
+  int t0;      // its first token
+  int n;       // its new tokens
+  int rb;      // row block within it
+  int split;   // chunk of its keys
+  int splits;  // chunks that the sequence's keys are cut into
+  int first;   // unit of the row block's first chunk
+  int64_t len;
   uint32_t chunk;
-  int active;
 };
-__device__ __forceinline__ Split split_keys(uint32_t kend, uint32_t splits) {
-  constexpr uint32_t step = ATT_WAVES * ATT_TILE;
-  uint32_t chunk = (kend + splits - 1) / splits;
-  chunk = (chunk + step - 1) / step * step;
-  if (chunk < ATT_MIN_CHUNK) chunk = ATT_MIN_CHUNK;
-  const uint32_t n = (kend + chunk - 1) / chunk;
-  return Split{chunk, int(n < 1 ? 1 : n)};
+
+// Tokens and keys of sequence b (no tokens where starts are out of order).
+struct Span {
+  int t0, n;
+  int64_t len;
+};
+__device__ __forceinline__ Span seq_span(const KvBatch& q, int64_t b) {
+  Span s{int(b), 0, 0};
+  if (b >= q.batch) return s;
+  s.len = q.lens[b];
+  s.n = 1;
+  if (q.starts) {
+    const int64_t t0 = q.starts[b], n = int64_t(q.starts[b + 1]) - t0;
+    const bool ok = n >= 0 && t0 >= 0 && t0 + n <= q.n_tokens;
+    s.t0 = ok ? int(t0) : 0;
+    s.n = ok ? int(n) : 0;
+  }
+  return s;
+}
+__device__ __forceinline__ uint32_t cached(int64_t len, int64_t cap) { return uint32_t(len < 0 ? 0 : len > cap ? cap : len); }
+
+// Inclusive prefix sums over the wave, by DPP adds: shifts by 1, 2, 4 and 8
+// within the rows of 16 lanes, then the rows' last sums to the rows behind.
+template <typename T, int CTRL, int ROWS>
+__device__ __forceinline__ T dpp_or_zero(T v) {
+  int w, r;
+  __builtin_memcpy(&w, &v, 4);
+  r = __builtin_amdgcn_update_dpp(0, w, CTRL, ROWS, 0xf, false);
+  __builtin_memcpy(&v, &r, 4);
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ T wave_prefix(T v) {
+  v += dpp_or_zero<T, 0x111, 0xf>(v);
+  v += dpp_or_zero<T, 0x112, 0xf>(v);
+  v += dpp_or_zero<T, 0x114, 0xf>(v);
+  v += dpp_or_zero<T, 0x118, 0xf>(v);
+  v += dpp_or_zero<T, 0x142, 0xa>(v);
+  v += dpp_or_zero<T, 0x143, 0xc>(v);
+  return v;
 }
 
-// A sequence's share of the new tokens. The launch has fewer than 2^24
-// 16-row blocks, so n * ratio fits 32 bits.
-struct Seq {
-  int b;   // sequence, -1: none
-  int t0;  // its first token
-  int n;   // its new tokens
-  int rb;  // row block within it
-};
-
-// The sequence and row block that workgroup number `at` works on. Uniform
-// over the wave, all of whose lanes take part.
-__device__ __forceinline__ Seq find_block(const KvBatch& q, int ratio, int at, int lane) {
-  if (!q.starts) {
-    const int per = int(row_blocks(1, ratio));
-    return Seq{at / per, at / per, 1, at % per};
+// The unit number `at` (JOIN = false), or the row block number `at` of those
+// with several units (JOIN = true). Uniform over the wave, all of whose lanes
+// take part.
+template <bool JOIN>
+__device__ __forceinline__ Seq find_unit(const AttArgs& a, int at, int lane) {
+  const KvBatch& q = a.b;
+  const int64_t cap = q.max_pages << a.c.shift;
+  Seq r{-1, 0, 0, 0, 0, 1, 0, 0, 0xFFFFFF80u};  // a chunk that holds any length
+  if (a.splits) {
+    float work = 0.0f;
+    for (int64_t b0 = 0; b0 < q.batch; b0 += 64) {
+      const Span s = seq_span(q, b0 + lane);
+      work += float(row_blocks(s.n, a.ratio)) * float(cached(s.len, cap));
+    }
+    work = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wave_prefix(work)), 63));
+    constexpr uint32_t step = ATT_WAVES * ATT_TILE;
+    const float share = fminf(work * float(a.c.heads) / float(a.target), 2.0e9f);
+    const uint32_t chunk = (uint32_t(share) + step) / step * step;
+    r.chunk = chunk < ATT_MIN_CHUNK ? ATT_MIN_CHUNK : chunk;
   }
-  int64_t before = 0;  // row blocks of the sequences passed
-  for (int b0 = 0; b0 < q.batch; b0 += 64) {
-    const int b = b0 + lane;
-    int64_t t0 = 0, n = 0;
-    if (b < q.batch) {
-      t0 = q.starts[b];
-      n = int64_t(q.starts[b + 1]) - t0;
-      if (n < 0 || t0 < 0 || t0 + n > q.n_tokens) n = 0;
-    }
-    const int64_t mine = row_blocks(n, ratio);
-    int64_t sum = mine;
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) {
-      const int64_t up = __shfl_up(sum, o);
-      if (lane >= o) sum += up;
-    }
-    const uint64_t past = __ballot(before + sum > at);
+  int before = 0, units_before = 0;  // of the sequences passed
+  for (int64_t b0 = 0; b0 < q.batch; b0 += 64) {
+    const Span s = seq_span(q, b0 + lane);
+    const uint32_t keys = cached(s.len, cap);
+    const int splits = a.splits && keys > r.chunk ? int((keys - 1) / r.chunk) + 1 : 1;
+    const int blocks = int(row_blocks(s.n, a.ratio));
+    // A sum past 2^24 is past the launch, whatever the arrays hold.
+    const int64_t all = int64_t(blocks) * splits;
+    const int units = int(all < (1 << 24) ? all : (1 << 24));
+    const int mine = !JOIN ? units : splits > 1 ? blocks : 0;
+    const int sum = wave_prefix(mine);
+    const int units_sum = JOIN ? wave_prefix(units) : sum;
+    const uint64_t past = __ballot(sum > at - before);
     if (past != 0) {
       const int src = __ffsll((unsigned long long)past) - 1;
-      const int first = int(before + __shfl(sum - mine, src));
-      return Seq{__builtin_amdgcn_readfirstlane(b0 + src), __builtin_amdgcn_readfirstlane(__shfl(int(t0), src)),
-                 __builtin_amdgcn_readfirstlane(__shfl(int(n), src)), __builtin_amdgcn_readfirstlane(at - first)};
+      const auto take = [&](int v) { return __builtin_amdgcn_readlane(v, src); };
+      r.b = int(b0) + src;
+      r.t0 = take(s.t0);
+      r.n = take(s.n);
+      r.len = take(int(s.len));
+      r.splits = take(splits);
+      const int n_blocks = take(blocks), k = at - before - take(sum - mine);
+      // The last row blocks see the most keys and come first.
+      const int back = JOIN ? k : k / r.splits;
+      r.rb = n_blocks - 1 - back;
+      r.split = JOIN ? 0 : k - back * r.splits;
+      r.first = units_before + take(units_sum - units) + back * r.splits;
+      return r;
     }
-    before += __shfl(sum, 63);
+    before += __builtin_amdgcn_readlane(sum, 63);
+    units_before += __builtin_amdgcn_readlane(units_sum, 63);
+    if (before > at || units_before > (1 << 24)) break;
   }
-  return Seq{-1, 0, 0, 0};
+  return r;
 }
 
 // Keys that new token i of n of a sequence of `len` tokens sees, `cap` of
@@ -263,6 +339,7 @@ template <int BITS, int DP, bool FULL, bool SPLIT>
 __global__ void __launch_bounds__(64 * ATT_WAVES, att_waves_per_simd(BITS, DP, SPLIT))
 kv_attend(AttArgs a) {
   using TL = Tile<BITS, DP>;
+  constexpr int BUFFERS = att_buffers(BITS, DP, SPLIT);
   constexpr int NJ = DP / 32, KW = TL::KW, DPL = TL::DPL, VW = TL::VW;
   constexpr float OFF = Half<BITS>::off;
   constexpr uint32_t MAGIC = Half<BITS>::magic;
@@ -273,19 +350,18 @@ kv_attend(AttArgs a) {
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int g = lane / 16, n16 = lane % 16;
   const int kv = int(blockIdx.x % unsigned(c.heads));
-  const Seq sq = find_block(a.b, a.ratio, int(blockIdx.x / unsigned(c.heads)), lane);
-  if (sq.b < 0 || sq.b >= a.b.batch) return;  // whole workgroup; uniform
+  const Seq sq = find_unit<false>(a, int(blockIdx.x / unsigned(c.heads)), lane);
+  if (sq.b < 0) return;  // whole workgroup; uniform
 
   const int64_t cap = a.b.max_pages << c.shift;
-  const int64_t len = __builtin_amdgcn_readfirstlane(a.b.lens[sq.b]);
+  const int64_t len = sq.len;
   const int last_row = block_last_row(sq.n, a.ratio, sq.rb);
   const int nrows = last_row - sq.rb * ATT_ROWS + 1;
   const uint32_t kend = keys_seen(len, sq.n, last_row / a.ratio, cap);
   if (len > cap && threadIdx.x == 0) kv_flag(a.info);
-  const Split sp = split_keys(kend, a.splits);
-  if (int(blockIdx.y) >= sp.active) return;
-  const uint32_t k0 = blockIdx.y * sp.chunk;
-  const uint32_t k1 = kend - k0 < sp.chunk ? kend : k0 + sp.chunk;
+  const uint32_t k0 = sq.split * sq.chunk;
+  if (sq.split > 0 && k0 >= kend) return;
+  const uint32_t k1 = kend - k0 < sq.chunk ? kend : k0 + sq.chunk;
 
   // This lane's query row, and the keys that every row of the block sees.
   const int row = sq.rb * ATT_ROWS + n16;
@@ -341,8 +417,7 @@ kv_attend(AttArgs a) {
   const uint32_t k_off = FULL ? 4u * (n16 * words + g * KW) : 4u * n16 * words;
   const uint32_t v_off = DPL * BITS == 16 ? 16u * g * words + 2u * vc : 16u * g * words + 4u * VW * vc;
   const auto blk = [&](int j) { return FULL ? g * NJ + j : 4 * j + g; };  // blocks of 8 d of this lane
-  TL t;
-  const auto load_keys = [&](const Rows& at) {
+  const auto load_keys = [&](const Rows& at, TL& t) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const char* kr = reinterpret_cast<const char*>(c.k_codes + at.at[u] * words);
@@ -359,7 +434,7 @@ kv_attend(AttArgs a) {
       if constexpr (SPLIT) t.kz[u] = *reinterpret_cast<const uint32_t*>(gr + 4u * n16);
     }
   };
-  const auto load_values = [&](const Rows& at) {
+  const auto load_values = [&](const Rows& at, TL& t) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       t.vg[u] = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(c.v_grid + at.at[u]) + 16u * g);
@@ -378,10 +453,11 @@ kv_attend(AttArgs a) {
   uint32_t p0 = k0 + wave * ATT_TILE;
   Rows at = {};
   Ids ids = look_up(p0);
+  TL first;
   if (p0 < k1) {
     at = locate(p0, ids);
-    load_keys(at);
-    load_values(at);
+    load_keys(at, first);
+    load_values(at, first);
     ids = look_up(p0 + step);
   }
 
@@ -432,9 +508,17 @@ kv_attend(AttArgs a) {
   float M = ATT_LOWEST, l = 0.0f;
   const Consts kc = conversion_consts<BITS>();
 
-  while (p0 < k1) {
+  // One tile, held in t; the next one's loads go to nx (with one buffer t
+  // itself, each part as soon as it has been used).
+  const auto tile = [&](TL& t, TL& nx) {
     const uint32_t ok = at.ok;
     const bool more = p0 + step < k1;
+    if (BUFFERS == 2 && more) {
+      at = locate(p0 + step, ids);
+      load_keys(at, nx);
+      load_values(at, nx);
+      ids = look_up(p0 + 2 * step);
+    }
     float x[8], sv[8];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -461,9 +545,9 @@ kv_attend(AttArgs a) {
         sv[4 * u + r] = kv_scale(vg[r]);
       }
     }
-    if (more) {
+    if (BUFFERS == 1 && more) {
       at = locate(p0 + step, ids);
-      load_keys(at);
+      load_keys(at, t);
       ids = look_up(p0 + 2 * step);
     }
     if (a.slopes) {
@@ -580,8 +664,18 @@ kv_attend(AttArgs a) {
         product(4 * vw + 3, h);
       }
     }
-    if (more) load_values(at);
+      if (BUFFERS == 1 && more) load_values(at, t);
     p0 += step;
+  };
+  if constexpr (BUFFERS == 2) {
+    TL second;
+    while (p0 < k1) {
+      tile(first, second);
+      if (p0 >= k1) break;
+      tile(second, first);
+    }
+  } else {
+    while (p0 < k1) tile(first, first);
   }
 
   // Join the waves: waves 0 and 1 leave their sums, waves 2 and 3 add theirs.
@@ -621,9 +715,8 @@ kv_attend(AttArgs a) {
     for (int w = 1; w < ATT_WAVES; ++w) top = fmaxf(top, lds_m[w][r]);
     float sum = 0.0f;
     for (int w = 0; w < ATT_WAVES; ++w) sum += lds_l[w][r] * __builtin_amdgcn_exp2f(lds_m[w][r] - top);
-    const int64_t heads_q = int64_t(c.heads) * a.ratio;
-    if (sp.active > 1) {
-      const int64_t pr = (int64_t(blockIdx.y) * a.b.n_tokens + t) * heads_q + h;
+    if (kend > sq.chunk) {  // one of several
+      const int64_t pr = (int64_t(sq.first + sq.split) * c.heads + kv) * a.rows + r;
       for (int d = lane; d < c.dim; d += 64)
         a.part_o[pr * c.dim + d] = lds_o[0][r][d] + lds_o[1][r][d];
       if (lane == 0) a.part_ml[pr] = float2{top, sum};
@@ -631,140 +724,123 @@ kv_attend(AttArgs a) {
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a row that sees no key gives zeros
       for (int d = lane; d < c.dim; d += 64) {
         const float v = (lds_o[0][r][d] + lds_o[1][r][d]) * inv;
-        const int64_t oo = t * a.ldo + int64_t(h) * c.dim + d;
-        if (a.out_dtype == GPTQ_F16)
-          static_cast<_Float16*>(a.out)[oo] = from_f32<_Float16>(v);
-        else if (a.out_dtype == GPTQ_BF16)
-          static_cast<bf16*>(a.out)[oo] = from_f32<bf16>(v);
-        else
-          static_cast<float*>(a.out)[oo] = v;
+        store_out(a, t * a.ldo + int64_t(h) * c.dim + d, v);
       }
     }
   }
 }
 
-// Joins the splits of one row (token, query head). Every thread holds 4 of
-// the row's d for one residue of the splits (lanes of a power of two cover
-// the row), so a row's splits are read 4 to 64 at a time; the sums of the
-// residues are added in order.
+// Joins the units of a row block's rows, in a fixed order: `rows` workgroups
+// share them. Every thread holds 4 of a row's d for one residue of the units
+// (lanes of a power of two cover the row), so 4 to 64 units are read at a
+// time, each thread rescaling its own sum as it goes; then the residues' sums
+// are added in order.
 __global__ void __launch_bounds__(64 * ATT_WAVES)
-kv_join(AttArgs a) {
-  __shared__ float weight[ATT_MAX_SPLITS];
+kv_join(AttArgs a, int rows) {
   __shared__ float4 sums[64 * ATT_WAVES];
+  __shared__ float tops[64], weights[64];
   const KvCache& c = a.c;
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int64_t heads_q = int64_t(c.heads) * a.ratio;
-  const int64_t t = int64_t(blockIdx.x) / heads_q;
-  const int h = int(int64_t(blockIdx.x) % heads_q);
-  // The token's sequence, and the keys of its row block as kv_attend took them.
-  int64_t b = t, t0 = t, n = 1;  // as in find_block
-  if (a.b.starts) {
-    int64_t cnt = 0;
-    for (int64_t i0 = 0; i0 <= a.b.batch; i0 += 64) {
-      const int64_t i = i0 + lane;
-      const uint64_t le = __ballot(i <= a.b.batch && int64_t(a.b.starts[i <= a.b.batch ? i : 0]) <= t);
-      cnt += __popcll(le);
-      if (le != ~uint64_t(0)) break;
-    }
-    b = cnt - 1;
-    if (b < 0 || b >= a.b.batch) return;
-    t0 = a.b.starts[b];
-    n = int64_t(a.b.starts[b + 1]) - t0;
-    if (n < 0 || t0 < 0 || t0 + n > a.b.n_tokens || t < t0 || t >= t0 + n) return;
-  }
-  const int64_t cap = a.b.max_pages << c.shift;
-  const int rb = (int(t - t0) * a.ratio + h % a.ratio) / ATT_ROWS;
-  const uint32_t kend = keys_seen(a.b.lens[b], int(n), block_last_row(int(n), a.ratio, rb) / a.ratio, cap);
-  const Split sp = split_keys(kend, a.splits);
-  if (sp.active <= 1) return;  // kv_attend wrote the row
-
-  const int64_t stride = a.b.n_tokens * heads_q, pr = t * heads_q + h;
-  // Each wave works out the weights of all splits, 64 at a time.
-  float top = ATT_LOWEST;
-  for (int s = lane; s < sp.active; s += 64) top = fmaxf(top, a.part_ml[s * stride + pr].x);
-#pragma unroll
-  for (int m = 1; m < 64; m *= 2) top = fmaxf(top, __shfl_xor(top, m));
-  float sum = 0.0f;
-  for (int s = lane; s < sp.active; s += 64) {
-    const float2 ml = a.part_ml[s * stride + pr];
-    const float f = __builtin_amdgcn_exp2f(ml.x - top);
-    if (wave == 0) weight[s] = f;
-    sum += ml.y * f;
-  }
-#pragma unroll
-  for (int m = 1; m < 64; m *= 2) sum += __shfl_xor(sum, m);
-  __syncthreads();
+  const int lane = threadIdx.x % 64;
+  const int kv = int(blockIdx.x / unsigned(rows) % unsigned(c.heads));
+  const Seq sq = find_unit<true>(a, int(blockIdx.x / unsigned(rows) / unsigned(c.heads)), lane);
+  if (sq.b < 0) return;
+  const int last_row = block_last_row(sq.n, a.ratio, sq.rb);
+  const uint32_t kend = keys_seen(sq.len, sq.n, last_row / a.ratio, a.b.max_pages << c.shift);
+  if (kend <= sq.chunk) return;  // kv_attend wrote the rows
+  const int active = int((kend - 1) / sq.chunk) + 1;
+  if (sq.first + active > a.units) return;  // only where starts are out of order
+  const int64_t stride = int64_t(c.heads) * a.rows;
   const int quads = c.dim / 4;
   const int per = quads <= 4 ? 4 : quads <= 8 ? 8 : quads <= 16 ? 16 : quads <= 32 ? 32 : 64;
   const int d4 = int(threadIdx.x) % per, residue = int(threadIdx.x) / per, residues = 64 * ATT_WAVES / per;
-  float4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (d4 < quads) {
-    const float4* src = reinterpret_cast<const float4*>(a.part_o) + pr * quads + d4;
+
+  for (int r = int(blockIdx.x % unsigned(rows)); r <= last_row - sq.rb * ATT_ROWS; r += rows) {
+    const int64_t pr = (int64_t(sq.first) * c.heads + kv) * a.rows + r;
+    const int row = sq.rb * ATT_ROWS + r;
+    const int64_t t = sq.t0 + row / a.ratio;
+    const int h = kv * a.ratio + row % a.ratio;
+    float4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    float top = ATT_LOWEST, sum = 0.0f;
+    const float4* src = reinterpret_cast<const float4*>(a.part_o) + pr * quads + (d4 < quads ? d4 : 0);
 #pragma unroll 4
-    for (int s = residue; s < sp.active; s += residues) {
+    for (int s = residue; s < active; s += residues) {
       const float4 v = src[s * stride * quads];
-      const float f = weight[s];
-      o.x = fmaf(v.x, f, o.x);
-      o.y = fmaf(v.y, f, o.y);
-      o.z = fmaf(v.z, f, o.z);
-      o.w = fmaf(v.w, f, o.w);
+      const float2 ml = a.part_ml[s * stride + pr];
+      const float m = fmaxf(top, ml.x);
+      const float f0 = __builtin_amdgcn_exp2f(top - m), f1 = __builtin_amdgcn_exp2f(ml.x - m);
+      top = m;
+      sum = fmaf(ml.y, f1, sum * f0);
+      o.x = fmaf(v.x, f1, o.x * f0);
+      o.y = fmaf(v.y, f1, o.y * f0);
+      o.z = fmaf(v.z, f1, o.z * f0);
+      o.w = fmaf(v.w, f1, o.w * f0);
     }
+    sums[threadIdx.x] = o;
+    if (d4 == 0) {
+      tops[residue] = top;
+      weights[residue] = sum;
+    }
+    __syncthreads();
+    const int d = int(threadIdx.x);
+    if (d < c.dim) {
+      const float* flat = reinterpret_cast<const float*>(sums);
+      const int used = active < residues ? active : residues;
+      top = tops[0];
+      for (int i = 1; i < used; ++i) top = fmaxf(top, tops[i]);
+      float v = 0.0f;
+      sum = 0.0f;
+      for (int i = 0; i < used; ++i) {
+        const float f = __builtin_amdgcn_exp2f(tops[i] - top);
+        v = fmaf(flat[i * per * 4 + d], f, v);
+        sum = fmaf(weights[i], f, sum);
+      }
+      v *= sum == 0.0f ? 0.0f : 1.0f / sum;
+      store_out(a, t * a.ldo + int64_t(h) * c.dim + d, v);
+    }
+    __syncthreads();  // the next row overwrites the sums
   }
-  sums[threadIdx.x] = o;
-  __syncthreads();
-  const int d = int(threadIdx.x);
-  if (d >= c.dim) return;
-  const float* flat = reinterpret_cast<const float*>(sums);
-  const int used = sp.active < residues ? sp.active : residues;
-  float v = 0.0f;
-  for (int r = 0; r < used; ++r) v += flat[r * per * 4 + d];
-  v *= sum == 0.0f ? 0.0f : 1.0f / sum;
-  const int64_t oo = t * a.ldo + int64_t(h) * c.dim + d;
-  if (a.out_dtype == GPTQ_F16)
-    static_cast<_Float16*>(a.out)[oo] = from_f32<_Float16>(v);
-  else if (a.out_dtype == GPTQ_BF16)
-    static_cast<bf16*>(a.out)[oo] = from_f32<bf16>(v);
-  else
-    static_cast<float*>(a.out)[oo] = v;
 }
 
-// Row blocks of a call (at most this many) times key-value heads.
-int64_t call_blocks(const KvCache& c, const KvBatch& b, int ratio) {
-  const int64_t rows = b.starts ? row_blocks(b.n_tokens, ratio) + b.batch : b.batch * row_blocks(1, ratio);
-  return rows * c.heads;
+// At most this many row blocks in a call (of each key-value head).
+int64_t call_blocks(const KvBatch& b, int ratio) {
+  return b.starts ? row_blocks(b.n_tokens, ratio) + b.batch : b.batch * row_blocks(1, ratio);
 }
-
-// Workgroups a row block's keys may be split over: enough of them to fill
-// the GPU, none with less than ATT_MIN_CHUNK of the table's keys.
-int call_splits(const KvCache& c, const KvBatch& b, int ratio) {
-  const int64_t blocks = call_blocks(c, b, ratio);
-  if (blocks < 1) return 1;
-  const int64_t keys = b.max_pages << c.shift;
-  int64_t s = (ATT_TARGET_GROUPS + blocks - 1) / blocks;
-  const int64_t most = (keys + ATT_MIN_CHUNK - 1) / ATT_MIN_CHUNK;
-  if (s > most) s = most;
-  if (s > ATT_MAX_SPLITS) s = ATT_MAX_SPLITS;
-  return int(s < 1 ? 1 : s);
+// At most this many units (see Seq).
+int64_t call_units(const KvCache& c, const KvBatch& b, int ratio, int target) {
+  const int64_t blocks = call_blocks(b, ratio), most = ((b.max_pages << c.shift) + ATT_MIN_CHUNK - 1) / ATT_MIN_CHUNK;
+  const int64_t spread = target / c.heads + 2 + blocks;
+  return spread / most < blocks ? spread : blocks * most;
 }
+int call_rows(const KvBatch& b, int ratio) { return b.starts || ratio > ATT_ROWS ? ATT_ROWS : ratio; }
 
 template <int BITS, int DP, bool FULL, bool SPLIT>
-int launch_attend(const AttArgs& a, dim3 grid, hipStream_t s) {
-  hipLaunchKernelGGL((kv_attend<BITS, DP, FULL, SPLIT>), grid, dim3(64 * ATT_WAVES), 0, s, a);
+int launch_attend(AttArgs& a, int64_t blocks, hipStream_t s) {
+  // One round of resident workgroups is what the keys are split for.
+  a.target = 256 * att_waves_per_simd(BITS, DP, SPLIT);
+  a.units = int(a.splits ? call_units(a.c, a.b, a.ratio, a.target) : blocks);
+  hipLaunchKernelGGL((kv_attend<BITS, DP, FULL, SPLIT>), dim3(unsigned(a.units * a.c.heads)), dim3(64 * ATT_WAVES), 0, s,
+                     a);
+  const int st = launch_status();
+  if (st != GPTQ_OK || !a.splits) return st;
+  // A row block with several units has more than the mean share of the work,
+  // so there are fewer than `target` of them (over all heads). Each gets a
+  // workgroup a row, or one for all where that would be very many.
+  const int64_t several = a.target / a.c.heads + 2, most = (several < blocks ? several : blocks) * a.c.heads;
+  const int rows = most * a.rows <= 4096 ? a.rows : 1;
+  hipLaunchKernelGGL(kv_join, dim3(unsigned(most * rows)), dim3(64 * ATT_WAVES), 0, s, a, rows);
   return launch_status();
 }
 template <int BITS, int DP>
-int launch_attend(const AttArgs& a, dim3 grid, bool split, hipStream_t s) {
+int launch_attend(AttArgs& a, int64_t blocks, bool split, hipStream_t s) {
   if (a.c.dim == DP)
-    return split ? launch_attend<BITS, DP, true, true>(a, grid, s)
-                 : launch_attend<BITS, DP, true, false>(a, grid, s);
-  return split ? launch_attend<BITS, DP, false, true>(a, grid, s)
-               : launch_attend<BITS, DP, false, false>(a, grid, s);
+    return split ? launch_attend<BITS, DP, true, true>(a, blocks, s) : launch_attend<BITS, DP, true, false>(a, blocks, s);
+  return split ? launch_attend<BITS, DP, false, true>(a, blocks, s) : launch_attend<BITS, DP, false, false>(a, blocks, s);
 }
 template <int BITS>
-int launch_attend(const AttArgs& a, dim3 grid, bool split, hipStream_t s) {
-  if (a.c.dim <= 64) return launch_attend<BITS, 64>(a, grid, split, s);
-  if (a.c.dim <= 128) return launch_attend<BITS, 128>(a, grid, split, s);
-  return launch_attend<BITS, 256>(a, grid, split, s);
+int launch_attend(AttArgs& a, int64_t blocks, bool split, hipStream_t s) {
+  if (a.c.dim <= 64) return launch_attend<BITS, 64>(a, blocks, split, s);
+  if (a.c.dim <= 128) return launch_attend<BITS, 128>(a, blocks, split, s);
+  return launch_attend<BITS, 256>(a, blocks, split, s);
 }
 
 }  // namespace
@@ -777,9 +853,11 @@ extern "C" size_t gptq_kv_attention_workspace_size(const gptq_kv_cache* cache, c
   KvCache c;
   KvBatch b;
   if (kv_views(cache, batch, &c, &b) != GPTQ_OK || q_heads < 1 || q_heads % c.heads != 0) return 0;
-  const int splits = call_splits(c, b, int(q_heads / c.heads));
-  if (splits <= 1) return 0;
-  return size_t(splits) * size_t(b.n_tokens) * size_t(q_heads) * (size_t(c.dim) * sizeof(float) + sizeof(float2));
+  const int ratio = int(q_heads / c.heads);
+  if (b.batch == 0 || b.n_tokens == 0) return 0;
+  const int64_t units = call_units(c, b, ratio, ATT_MAX_TARGET);
+  if (units <= call_blocks(b, ratio)) return 0;  // one unit each
+  return size_t(units) * size_t(c.heads) * size_t(call_rows(b, ratio)) * (size_t(c.dim) * sizeof(float) + sizeof(float2));
 }
 
 extern "C" int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const void* q, int q_dtype,
@@ -799,8 +877,10 @@ extern "C" int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch
     return GPTQ_E_INVALID_ARG;
   if (a.b.n_tokens == 0 || a.b.batch == 0) return GPTQ_OK;
   a.ratio = int(q_heads / a.c.heads);
-  const int64_t blocks = call_blocks(a.c, a.b, a.ratio);
-  if (blocks >= (int64_t(1) << 24) || a.b.n_tokens * q_heads >= (int64_t(1) << 31)) return GPTQ_E_INVALID_ARG;
+  const int64_t blocks = call_blocks(a.b, a.ratio), units = call_units(a.c, a.b, a.ratio, ATT_MAX_TARGET);
+  a.rows = call_rows(a.b, a.ratio);
+  a.splits = units > blocks;
+  if (units * a.c.heads >= (int64_t(1) << 24)) return GPTQ_E_INVALID_ARG;
   a.q = q;
   a.out = out;
   a.slopes = slopes;
@@ -811,18 +891,13 @@ extern "C" int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch
   a.q_dtype = q_dtype;
   a.out_dtype = out_dtype;
   a.q_vec = kv_vec16(q, ldq, q_dtype);
-  a.splits = call_splits(a.c, a.b, a.ratio);
-  if (a.splits > 1) {
+  if (a.splits) {
     if (ws_bytes < gptq_kv_attention_workspace_size(cache, batch, q_heads)) return GPTQ_E_WORKSPACE;
     if (!ws || reinterpret_cast<uintptr_t>(ws) % 16 != 0) return GPTQ_E_INVALID_ARG;
     a.part_o = static_cast<float*>(ws);  // its rows stay 16-byte aligned: head_dim is a multiple of 16
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + int64_t(a.splits) * a.b.n_tokens * q_heads * a.c.dim);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + units * a.c.heads * a.rows * a.c.dim);
   }
   const bool split = q_dtype == GPTQ_F32 || out_dtype == GPTQ_F32;
-  const dim3 grid(unsigned(blocks), unsigned(a.splits));
   hipStream_t s = as_stream(stream);
-  st = cache->bits == 4 ? launch_attend<4>(a, grid, split, s) : launch_attend<8>(a, grid, split, s);
-  if (st != GPTQ_OK || a.splits == 1) return st;
-  hipLaunchKernelGGL(kv_join, dim3(unsigned(a.b.n_tokens * q_heads)), dim3(64 * ATT_WAVES), 0, s, a);
-  return launch_status();
+  return cache->bits == 4 ? launch_attend<4>(a, blocks, split, s) : launch_attend<8>(a, blocks, split, s);
 }

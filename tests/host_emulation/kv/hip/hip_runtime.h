@@ -107,6 +107,19 @@ inline int dpp_source(int lane, int ctrl) {
   std::abort();
 }
 
+// A DPP move that keeps `old` where the source lane is outside its row, where
+// a row has nothing broadcast to it, or where the row mask excludes it.
+inline int update_dpp(int old, int src, int ctrl, int row_mask, int bank_mask) {
+  const int64_t* v = exchange(src);
+  const int l = my_lane(), row = l / 16, r = l % 16;
+  if (bank_mask != 0xf) std::abort();
+  if (!(row_mask >> row & 1)) return old;
+  if (ctrl >= 0x111 && ctrl <= 0x11F) return r >= ctrl - 0x110 ? int(v[l - (ctrl - 0x110)]) : old;  // row_shr
+  if (ctrl == 0x142) return row > 0 ? int(v[16 * row - 1]) : old;                                   // row_bcast:15
+  if (ctrl == 0x143) return l >= 32 ? int(v[31]) : old;                                             // row_bcast:31
+  return int(v[dpp_source(l, ctrl)]);
+}
+
 // v_mfma_f32_16x16x32_f16: lane l holds A[l % 16][8 (l / 16) + j] and
 // B[8 (l / 16) + j][l % 16], j = 0..7; it returns D[4 (l / 16) + r][l % 16].
 inline floatx4_t mfma_16x16x32(half8_t a, half8_t b, floatx4_t c) {
@@ -210,8 +223,9 @@ inline T __shfl(T v, int src) {
   return simt::from_lane(v, src);
 }
 
-#define __builtin_amdgcn_update_dpp(old, src, ctrl, rm, bm, bc) simt::from_lane((src), simt::dpp_source(simt::my_lane(), (ctrl)))
+#define __builtin_amdgcn_update_dpp(old, src, ctrl, rm, bm, bc) simt::update_dpp((old), (src), (ctrl), (rm), (bm))
 #define __builtin_amdgcn_mov_dpp(src, ctrl, rm, bm, bc) simt::from_lane((src), simt::dpp_source(simt::my_lane(), (ctrl)))
+#define __builtin_amdgcn_readlane(v, src) simt::from_lane((v), (src))
 #define __builtin_amdgcn_readfirstlane(v) simt::from_lane((v), 0)
 #define __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, cbsz, abid, blgp) simt::mfma_16x16x32((a), (b), (c))
 #define __builtin_amdgcn_perm(s0, s1, sel) simt::perm((s0), (s1), (sel))
