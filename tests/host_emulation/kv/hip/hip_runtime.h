@@ -229,6 +229,8 @@ inline T __shfl(T v, int src) {
 #define __builtin_amdgcn_readfirstlane(v) simt::from_lane((v), 0)
 #define __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, cbsz, abid, blgp) simt::mfma_16x16x32((a), (b), (c))
 #define __builtin_amdgcn_perm(s0, s1, sel) simt::perm((s0), (s1), (sel))
+#define __builtin_amdgcn_rcpf(x) (1.0f / (x))
+#define __builtin_amdgcn_fmed3f(x, lo, hi) std::fmax(std::fmin((x), (hi)), (lo))
 #define __builtin_amdgcn_exp2f(x) std::exp2f(x)
 #define __builtin_amdgcn_logf(x) std::log2f(x)
 
