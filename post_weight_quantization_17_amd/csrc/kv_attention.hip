@@ -37,268 +37,15 @@
 // through LDS; where the rows alone do not fill the GPU, a row block's keys
 // are split over workgroups too, whose partial sums kv_join adds in a fixed
 // order. Each partial result has its M; all reductions are fp32.
-#include "kv_cache.h"
+#include "kv_attention.h"
 
 namespace gptq {
 namespace {
-
-constexpr int ATT_WAVES = 4;
-constexpr int ATT_ROWS = 16;                     // query rows of a workgroup
-constexpr int ATT_TILE = 32;                     // keys a wave takes at a time
-constexpr int ATT_MIN_CHUNK = 256;               // fewest keys of a workgroup when a row's keys are split
-constexpr int ATT_MAX_TARGET = 4 * 256;          // most workgroups that the keys are split for (Seq)
-constexpr float ATT_W_TOP = 8.0f;                // log2 of the largest weight after a rescaling
-constexpr float ATT_W_LIMIT = 32768.0f;          // a weight above this asks for the next one
-constexpr float ATT_LOWEST = -3.402823466e38f;   // M before the first key
-constexpr float LOG2E = 1.44269504088896340736f;
-
-struct AttArgs {
-  KvCache c;
-  KvBatch b;
-  const void* q;
-  void* out;
-  const float* slopes;
-  float* part_o;    // [units][kv_heads][rows][dim]: a unit's partial sums
-  float2* part_ml;  // [units][kv_heads][rows]: their reference and weight sum
-  int32_t* info;
-  int64_t ldq, ldo;
-  float scale;  // of the scores, in log2 units
-  int ratio;    // query heads that share a key-value head
-  int q_dtype, out_dtype, q_vec;
-  int rows;     // rows of a unit in the workspace
-  int splits;   // 0: no row block's keys are split
-  int units;    // of the launch
-  int target;   // workgroups that the keys are split for
-};
 
 // Waves that share a SIMD: as many as the registers of a form leave without
 // spilling (a tile in flight and one in work, the sums of DP / 16 MFMAs).
 constexpr int att_waves_per_simd(int bits, int dp, bool split) {
   return dp == 256 ? (bits == 8 && split ? 1 : 2) : dp == 128 ? (bits == 8 && split ? 2 : 3) : (split ? 3 : 4);
-}
-
-constexpr int att_buffers(int bits, int dp, bool split) { return 1; }
-
-__device__ __forceinline__ void store_out(const AttArgs& a, int64_t at, float v) {
-  if (a.out_dtype == GPTQ_F16)
-    static_cast<_Float16*>(a.out)[at] = from_f32<_Float16>(v);
-  else if (a.out_dtype == GPTQ_BF16)
-    static_cast<bf16*>(a.out)[at] = from_f32<bf16>(v);
-  else
-    static_cast<float*>(a.out)[at] = v;
-}
-
-// The row blocks of a sequence with n new tokens.
-__host__ __device__ __forceinline__ int64_t row_blocks(int64_t n, int ratio) {
-  return (n * ratio + ATT_ROWS - 1) / ATT_ROWS;
-}
-
-// A call's work is cut into units: one row block (of one key-value head) over
-// one chunk of its sequence's keys. The chunk is the same for all sequences,
-// so that units take about the same time however ragged the batch is: the
-// keys of all row blocks over the workgroups that the GPU is to be filled
-// with, in whole tiles of the 4 waves. Lengths are device data, so every
-// workgroup works the chunk out for itself, from the same numbers in the same
-// order. A sequence has ceil(len / chunk) units a row block (at least one,
-// which writes the zeros of rows without keys); those past a causal row
-// block's last key have nothing to do.
-//
-// The host's bound of the units (call_units) holds because each sequence has
-// at most len / chunk + 1 a row block, and chunk is at least the mean share.
-// The launch has fewer than 2^24 row blocks, so n * ratio fits 32 bits;
-// lengths are int32, so positions and their sums here do, too.
-struct Seq {
-  int b;       // sequence, -1: none
-  int t0;      // its first token
-  int n;       // its new tokens
-  int rb;      // row block within it
-  int split;   // chunk of its keys
-  int splits;  // chunks that the sequence's keys are cut into
-  int first;   // unit of the row block's first chunk
-  int64_t len;
-  uint32_t chunk;
-};
-
-// Tokens and keys of sequence b (no tokens where starts are out of order).
-struct Span {
-  int t0, n;
-  int64_t len;
-};
-__device__ __forceinline__ Span seq_span(const KvBatch& q, int64_t b) {
-  Span s{int(b), 0, 0};
-  if (b >= q.batch) return s;
-  s.len = q.lens[b];
-  s.n = 1;
-  if (q.starts) {
-    const int64_t t0 = q.starts[b], n = int64_t(q.starts[b + 1]) - t0;
-    const bool ok = n >= 0 && t0 >= 0 && t0 + n <= q.n_tokens;
-    s.t0 = ok ? int(t0) : 0;
-    s.n = ok ? int(n) : 0;
-  }
-  return s;
-}
-__device__ __forceinline__ uint32_t cached(int64_t len, int64_t cap) { return uint32_t(len < 0 ? 0 : len > cap ? cap : len); }
-
-// Inclusive prefix sums over the wave, by DPP adds: shifts by 1, 2, 4 and 8
-// within the rows of 16 lanes, then the rows' last sums to the rows behind.
-template <typename T, int CTRL, int ROWS>
-__device__ __forceinline__ T dpp_or_zero(T v) {
-  int w, r;
-  __builtin_memcpy(&w, &v, 4);
-  r = __builtin_amdgcn_update_dpp(0, w, CTRL, ROWS, 0xf, false);
-  __builtin_memcpy(&v, &r, 4);
-  return v;
-}
-template <typename T>
-__device__ __forceinline__ T wave_prefix(T v) {
-  v += dpp_or_zero<T, 0x111, 0xf>(v);
-  v += dpp_or_zero<T, 0x112, 0xf>(v);
-  v += dpp_or_zero<T, 0x114, 0xf>(v);
-  v += dpp_or_zero<T, 0x118, 0xf>(v);
-  v += dpp_or_zero<T, 0x142, 0xa>(v);
-  v += dpp_or_zero<T, 0x143, 0xc>(v);
-  return v;
-}
-
-// The unit number `at` (JOIN = false), or the row block number `at` of those
-// with several units (JOIN = true). Uniform over the wave, all of whose lanes
-// take part.
-template <bool JOIN>
-__device__ __forceinline__ Seq find_unit(const AttArgs& a, int at, int lane) {
-  const KvBatch& q = a.b;
-  const int64_t cap = q.max_pages << a.c.shift;
-  Seq r{-1, 0, 0, 0, 0, 1, 0, 0, 0xFFFFFF80u};  // a chunk that holds any length
-  if (a.splits) {
-    float work = 0.0f;
-    for (int64_t b0 = 0; b0 < q.batch; b0 += 64) {
-      const Span s = seq_span(q, b0 + lane);
-      work += float(row_blocks(s.n, a.ratio)) * float(cached(s.len, cap));
-    }
-    work = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wave_prefix(work)), 63));
-    constexpr uint32_t step = ATT_WAVES * ATT_TILE;
-    const float share = fminf(work * float(a.c.heads) / float(a.target), 2.0e9f);
-    const uint32_t chunk = (uint32_t(share) + step) / step * step;
-    r.chunk = chunk < ATT_MIN_CHUNK ? ATT_MIN_CHUNK : chunk;
-  }
-  int before = 0, units_before = 0;  // of the sequences passed
-  for (int64_t b0 = 0; b0 < q.batch; b0 += 64) {
-    const Span s = seq_span(q, b0 + lane);
-    const uint32_t keys = cached(s.len, cap);
-    const int splits = a.splits && keys > r.chunk ? int((keys - 1) / r.chunk) + 1 : 1;
-    const int blocks = int(row_blocks(s.n, a.ratio));
-    // A sum past 2^24 is past the launch, whatever the arrays hold.
-    const int64_t all = int64_t(blocks) * splits;
-    const int units = int(all < (1 << 24) ? all : (1 << 24));
-    const int mine = !JOIN ? units : splits > 1 ? blocks : 0;
-    const int sum = wave_prefix(mine);
-    const int units_sum = JOIN ? wave_prefix(units) : sum;
-    const uint64_t past = __ballot(sum > at - before);
-    if (past != 0) {
-      const int src = __ffsll((unsigned long long)past) - 1;
-      const auto take = [&](int v) { return __builtin_amdgcn_readlane(v, src); };
-      r.b = int(b0) + src;
-      r.t0 = take(s.t0);
-      r.n = take(s.n);
-      r.len = take(int(s.len));
-      r.splits = take(splits);
-      const int n_blocks = take(blocks), k = at - before - take(sum - mine);
-      // The last row blocks see the most keys and come first.
-      const int back = JOIN ? k : k / r.splits;
-      r.rb = n_blocks - 1 - back;
-      r.split = JOIN ? 0 : k - back * r.splits;
-      r.first = units_before + take(units_sum - units) + back * r.splits;
-      return r;
-    }
-    before += __builtin_amdgcn_readlane(sum, 63);
-    units_before += __builtin_amdgcn_readlane(units_sum, 63);
-    if (before > at || units_before > (1 << 24)) break;
-  }
-  return r;
-}
-
-// Keys that new token i of n of a sequence of `len` tokens sees, `cap` of
-// which the table reaches.
-__device__ __forceinline__ uint32_t keys_seen(int64_t len, int n, int i, int64_t cap) {
-  const int64_t end = len - n + i + 1;
-  return uint32_t(end < 0 ? 0 : end > cap ? cap : end);
-}
-__device__ __forceinline__ int block_last_row(int n, int ratio, int rb) {
-  const int last = rb * ATT_ROWS + ATT_ROWS - 1, rows = n * ratio;
-  return last < rows ? last : rows - 1;
-}
-
-__device__ __forceinline__ uint32_t as_u32(half2v v) {
-  uint32_t r;
-  __builtin_memcpy(&r, &v, 4);
-  return r;
-}
-__device__ __forceinline__ half2v as_half2(uint32_t v) {
-  half2v r;
-  __builtin_memcpy(&r, &v, 4);
-  return r;
-}
-__device__ __forceinline__ half8 as_half8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  const uint32_t w[4] = {a, b, c, d};
-  half8 r;
-  __builtin_memcpy(&r, w, 16);
-  return r;
-}
-
-// What a code is offset by in its fp16 half, the bits of that half, and the
-// position of the code in it.
-template <int BITS>
-struct Half {
-  static constexpr float off = BITS == 4 ? 64.0f : 1024.0f;
-  static constexpr uint32_t magic = BITS == 4 ? 0x54005400u : 0x64006400u;
-  static constexpr int at = BITS == 4 ? 4 : 0;
-};
-
-// The conversion's constants, kept in registers: a mask in an SGPR and the
-// exponent pattern in a VGPR make mask-and-merge one v_and_or_b32, which
-// takes no literals.
-struct Consts {
-  uint32_t mask, magic;
-};
-template <int BITS>
-__device__ __forceinline__ Consts conversion_consts() {
-  Consts k{0x00F000F0u, Half<BITS>::magic};
-  KV_OPAQUE_S(k.mask);
-  KV_OPAQUE_V(k.magic);
-  return k;
-}
-
-// 4-bit codes: code i (0..3) of each 16-bit half of w, as two halves 64 + c.
-template <int I>
-__device__ __forceinline__ uint32_t nibbles(uint32_t w, const Consts& k) {
-  constexpr int up = 4 - 4 * I;
-  return ((up > 0 ? w << up : w >> -up) & k.mask) | k.magic;
-}
-// 8-bit codes: bytes A and B of w, as two halves 1024 + c.
-template <int A, int B>
-__device__ __forceinline__ uint32_t byte_pair(uint32_t w, const Consts& k) {
-  return __builtin_amdgcn_perm(k.magic, w, 0x05000500u | A | B << 16);
-}
-
-// The 8 codes of a lane's k-slots in one MFMA of the first product. 4 bits:
-// one word, in the order 0 4 1 5 2 6 3 7; 8 bits: two words, in order.
-template <int BITS>
-struct KeyOrder {
-  static constexpr int code(int i) { return BITS == 4 ? (i % 2) * 4 + i / 2 : i; }
-};
-template <int BITS>
-__device__ __forceinline__ void key_codes(const uint32_t* w, uint32_t (&h)[4], const Consts& k) {
-  if constexpr (BITS == 4) {
-    h[0] = nibbles<0>(w[0], k);
-    h[1] = nibbles<1>(w[0], k);
-    h[2] = nibbles<2>(w[0], k);
-    h[3] = nibbles<3>(w[0], k);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      h[2 * i] = byte_pair<0, 1>(w[i], k);
-      h[2 * i + 1] = byte_pair<2, 3>(w[i], k);
-    }
-  }
 }
 
 // A lane's share of one 32-key tile, as loaded.
@@ -313,33 +60,10 @@ struct Tile {
   uint32_t kz[2];
 };
 
-// N words at p, which is aligned to the largest power of two that divides
-// their size, 16 bytes at most.
-template <int N>
-__device__ __forceinline__ void load_words(const char* p, uint32_t* w) {
-  if constexpr (N % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-    }
-  } else if constexpr (N % 2 == 0) {
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      const uint2 v = reinterpret_cast<const uint2*>(p)[i];
-      w[2 * i] = v.x, w[2 * i + 1] = v.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
-  }
-}
-
 template <int BITS, int DP, bool FULL, bool SPLIT>
 __global__ void __launch_bounds__(64 * ATT_WAVES, att_waves_per_simd(BITS, DP, SPLIT))
 kv_attend(AttArgs a) {
   using TL = Tile<BITS, DP>;
-  constexpr int BUFFERS = att_buffers(BITS, DP, SPLIT);
   constexpr int NJ = DP / 32, KW = TL::KW, DPL = TL::DPL, VW = TL::VW;
   constexpr float OFF = Half<BITS>::off;
   constexpr uint32_t MAGIC = Half<BITS>::magic;
@@ -355,7 +79,7 @@ kv_attend(AttArgs a) {
 
   const int64_t cap = a.b.max_pages << c.shift;
   const int64_t len = sq.len;
-  const int last_row = block_last_row(sq.n, a.ratio, sq.rb);
+  const int last_row = block_last_row(a, sq.n, sq.rb);
   const int nrows = last_row - sq.rb * ATT_ROWS + 1;
   const uint32_t kend = keys_seen(len, sq.n, last_row / a.ratio, cap);
   if (len > cap && threadIdx.x == 0) kv_flag(a.info);
@@ -416,8 +140,9 @@ kv_attend(AttArgs a) {
   const int vc = n16 * DPL < c.dim ? n16 : 0;  // lanes past the head's end repeat the first one's codes
   const uint32_t k_off = FULL ? 4u * (n16 * words + g * KW) : 4u * n16 * words;
   const uint32_t v_off = DPL * BITS == 16 ? 16u * g * words + 2u * vc : 16u * g * words + 4u * VW * vc;
-  const auto blk = [&](int j) { return FULL ? g * NJ + j : 4 * j + g; };  // blocks of 8 d of this lane
-  const auto load_keys = [&](const Rows& at, TL& t) {
+  const auto blk = [&](int j) { return lane_block<DP, FULL>(g, j); };
+  TL t;
+  const auto load_keys = [&](const Rows& at) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const char* kr = reinterpret_cast<const char*>(c.k_codes + at.at[u] * words);
@@ -434,7 +159,7 @@ kv_attend(AttArgs a) {
       if constexpr (SPLIT) t.kz[u] = *reinterpret_cast<const uint32_t*>(gr + 4u * n16);
     }
   };
-  const auto load_values = [&](const Rows& at, TL& t) {
+  const auto load_values = [&](const Rows& at) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       t.vg[u] = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(c.v_grid + at.at[u]) + 16u * g);
@@ -453,54 +178,15 @@ kv_attend(AttArgs a) {
   uint32_t p0 = k0 + wave * ATT_TILE;
   Rows at = {};
   Ids ids = look_up(p0);
-  TL first;
   if (p0 < k1) {
     at = locate(p0, ids);
-    load_keys(at, first);
-    load_values(at, first);
+    load_keys(at);
+    load_values(at);
     ids = look_up(p0 + step);
   }
 
-  // Queries: block j of 8 elements of this lane, in the order of the codes.
-  half8 qh[NJ], ql[NJ];
-  float qsum = 0.0f, row_scale;
-  {
-    float f[NJ][8];
-    float top = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[j][e] = 0.0f;
-      const int d0 = 8 * blk(j);
-      if (live && d0 < c.dim) {
-        const int64_t at = int64_t(sq.t0 + i) * a.ldq + int64_t(hq) * c.dim + d0;
-        if (a.q_dtype == GPTQ_F16)
-          load8(static_cast<const _Float16*>(a.q) + at, a.q_vec, f[j]);
-        else if (a.q_dtype == GPTQ_BF16)
-          load8(static_cast<const bf16*>(a.q) + at, a.q_vec, f[j]);
-        else
-          load8(static_cast<const float*>(a.q) + at, a.q_vec, f[j]);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[j][e]));
-    }
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    int ex = int(__float_as_uint(top) >> 23) - 127;
-    if (ex > 127 || top == 0.0f) ex = 13;  // nothing to scale, or an infinity
-    row_scale = ldexpf(a.scale, ex - 13);
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float s = ldexpf(f[j][KeyOrder<BITS>::code(e)], 13 - ex);
-        qh[j][e] = _Float16(s);
-        qsum += float(qh[j][e]);
-        if constexpr (SPLIT) ql[j][e] = _Float16(s - float(qh[j][e]));
-      }
-    qsum += __shfl_xor(qsum, 16);
-    qsum += __shfl_xor(qsum, 32);
-  }
+  Query<BITS, DP, FULL, SPLIT> q;
+  q.load(a, live, sq.t0 + i, hq, g);
 
   floatx4 o[DPL];
 #pragma unroll
@@ -508,17 +194,9 @@ kv_attend(AttArgs a) {
   float M = ATT_LOWEST, l = 0.0f;
   const Consts kc = conversion_consts<BITS>();
 
-  // One tile, held in t; the next one's loads go to nx (with one buffer t
-  // itself, each part as soon as it has been used).
-  const auto tile = [&](TL& t, TL& nx) {
+  while (p0 < k1) {
     const uint32_t ok = at.ok;
     const bool more = p0 + step < k1;
-    if (BUFFERS == 2 && more) {
-      at = locate(p0 + step, ids);
-      load_keys(at, nx);
-      load_values(at, nx);
-      ids = look_up(p0 + 2 * step);
-    }
     float x[8], sv[8];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -533,21 +211,21 @@ kv_attend(AttArgs a) {
           for (int e = 0; e < 4; ++e) h[e] = as_u32(as_half2(h[e]) - as_half2(z1));
         }
         const half8 keys = as_half8(h[0], h[1], h[2], h[3]);
-        if constexpr (SPLIT) acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(keys, ql[j], acc, 0, 0, 0);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(keys, qh[j], acc, 0, 0, 0);
+        if constexpr (SPLIT) acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(keys, q.l[j], acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(keys, q.h[j], acc, 0, 0, 0);
       }
       const uint32_t kg[4] = {t.kg[u].x, t.kg[u].y, t.kg[u].z, t.kg[u].w};
       const uint32_t vg[4] = {t.vg[u].x, t.vg[u].y, t.vg[u].z, t.vg[u].w};
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float s = kv_scale(kg[r]) * row_scale;
-        x[4 * u + r] = SPLIT ? acc[r] * s : fmaf(-(OFF + float(kv_zero<BITS>(kg[r]))), qsum, acc[r]) * s;
+        const float s = kv_scale(kg[r]) * q.scale;
+        x[4 * u + r] = SPLIT ? acc[r] * s : fmaf(-(OFF + float(kv_zero<BITS>(kg[r]))), q.sum, acc[r]) * s;
         sv[4 * u + r] = kv_scale(vg[r]);
       }
     }
-    if (BUFFERS == 1 && more) {
+    if (more) {
       at = locate(p0 + step, ids);
-      load_keys(at, t);
+      load_keys(at);
       ids = look_up(p0 + 2 * step);
     }
     if (a.slopes) {
@@ -664,18 +342,8 @@ kv_attend(AttArgs a) {
         product(4 * vw + 3, h);
       }
     }
-      if (BUFFERS == 1 && more) load_values(at, t);
+      if (more) load_values(at);
     p0 += step;
-  };
-  if constexpr (BUFFERS == 2) {
-    TL second;
-    while (p0 < k1) {
-      tile(first, second);
-      if (p0 >= k1) break;
-      tile(second, first);
-    }
-  } else {
-    while (p0 < k1) tile(first, first);
   }
 
   // Join the waves: waves 0 and 1 leave their sums, waves 2 and 3 add theirs.
@@ -716,6 +384,7 @@ kv_attend(AttArgs a) {
     float sum = 0.0f;
     for (int w = 0; w < ATT_WAVES; ++w) sum += lds_l[w][r] * __builtin_amdgcn_exp2f(lds_m[w][r] - top);
     if (kend > sq.chunk) {  // one of several
+      if (sq.first + sq.split >= a.parts) break;  // only where starts are out of order
       const int64_t pr = (int64_t(sq.first + sq.split) * c.heads + kv) * a.rows + r;
       for (int d = lane; d < c.dim; d += 64)
         a.part_o[pr * c.dim + d] = lds_o[0][r][d] + lds_o[1][r][d];
@@ -744,19 +413,19 @@ kv_join(AttArgs a, int rows) {
   const int kv = int(blockIdx.x / unsigned(rows) % unsigned(c.heads));
   const Seq sq = find_unit<true>(a, int(blockIdx.x / unsigned(rows) / unsigned(c.heads)), lane);
   if (sq.b < 0) return;
-  const int last_row = block_last_row(sq.n, a.ratio, sq.rb);
+  const int last_row = block_last_row(a, sq.n, sq.rb);
   const uint32_t kend = keys_seen(sq.len, sq.n, last_row / a.ratio, a.b.max_pages << c.shift);
   if (kend <= sq.chunk) return;  // kv_attend wrote the rows
   const int active = int((kend - 1) / sq.chunk) + 1;
-  if (sq.first + active > a.units) return;  // only where starts are out of order
+  if (sq.first + active > a.parts) return;  // only where starts are out of order
   const int64_t stride = int64_t(c.heads) * a.rows;
   const int quads = c.dim / 4;
   const int per = quads <= 4 ? 4 : quads <= 8 ? 8 : quads <= 16 ? 16 : quads <= 32 ? 32 : 64;
   const int d4 = int(threadIdx.x) % per, residue = int(threadIdx.x) / per, residues = 64 * ATT_WAVES / per;
 
-  for (int r = int(blockIdx.x % unsigned(rows)); r <= last_row - sq.rb * ATT_ROWS; r += rows) {
+  for (int r = int(blockIdx.x % unsigned(rows)); r <= last_row - sq.rb * a.block_rows; r += rows) {
     const int64_t pr = (int64_t(sq.first) * c.heads + kv) * a.rows + r;
-    const int row = sq.rb * ATT_ROWS + r;
+    const int row = sq.rb * a.block_rows + r;
     const int64_t t = sq.t0 + row / a.ratio;
     const int h = kv * a.ratio + row % a.ratio;
     float4 o = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -801,46 +470,52 @@ kv_join(AttArgs a, int rows) {
   }
 }
 
-// At most this many row blocks in a call (of each key-value head).
-int64_t call_blocks(const KvBatch& b, int ratio) {
-  return b.starts ? row_blocks(b.n_tokens, ratio) + b.batch : b.batch * row_blocks(1, ratio);
+// How a call is cut: everything that does not depend on device data, nor on
+// the types (workspace sizes are asked for without them).
+struct Cut {
+  bool prompt;     // by the prompts' kernel
+  int block_rows;  // query rows of a row block
+  int rows;        // most of them in any
+  int64_t blocks;  // at most this many row blocks (of each key-value head)
+  int64_t chunks;  // at most this many chunks of any sequence's keys
+  int64_t parts;   // at most this many partial results
+};
+Cut cut_call(const KvCache& c, const KvBatch& b, int ratio) {
+  Cut k;
+  // The prompts' kernel converts the cache once for 4 waves of rows; it takes
+  // the calls whose sequences have PROMPT_ROWS query rows in the mean.
+  k.prompt = b.starts && b.n_tokens * ratio >= PROMPT_ROWS * b.batch;
+  k.block_rows = k.prompt ? prompt_rows(c.dim) : ATT_ROWS;
+  k.rows = b.starts || ratio > k.block_rows ? k.block_rows : ratio;
+  k.blocks = b.starts ? row_blocks(b.n_tokens, ratio, k.block_rows) + b.batch : b.batch * row_blocks(1, ratio, k.block_rows);
+  k.chunks = ((b.max_pages << c.shift) + ATT_MIN_CHUNK - 1) / ATT_MIN_CHUNK;
+  const int64_t parts = 2 * (k.prompt ? PROMPT_MAX_TARGET : ATT_MAX_TARGET) / c.heads + 2;
+  k.parts = k.chunks <= 1 ? 0 : parts / k.chunks < k.blocks ? parts : k.blocks * k.chunks;
+  return k;
 }
 // At most this many units (see Seq).
-int64_t call_units(const KvCache& c, const KvBatch& b, int ratio, int target) {
-  const int64_t blocks = call_blocks(b, ratio), most = ((b.max_pages << c.shift) + ATT_MIN_CHUNK - 1) / ATT_MIN_CHUNK;
-  const int64_t spread = target / c.heads + 2 + blocks;
-  return spread / most < blocks ? spread : blocks * most;
+int64_t call_units(const Cut& k, int heads, int target) {
+  const int64_t spread = target / heads + 2 + k.blocks;
+  return spread / k.chunks < k.blocks ? spread : k.blocks * k.chunks;
 }
-int call_rows(const KvBatch& b, int ratio) { return b.starts || ratio > ATT_ROWS ? ATT_ROWS : ratio; }
 
 template <int BITS, int DP, bool FULL, bool SPLIT>
-int launch_attend(AttArgs& a, int64_t blocks, hipStream_t s) {
-  // One round of resident workgroups is what the keys are split for.
-  a.target = 256 * att_waves_per_simd(BITS, DP, SPLIT);
-  a.units = int(a.splits ? call_units(a.c, a.b, a.ratio, a.target) : blocks);
+int launch_attend(const AttArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((kv_attend<BITS, DP, FULL, SPLIT>), dim3(unsigned(a.units * a.c.heads)), dim3(64 * ATT_WAVES), 0, s,
                      a);
-  const int st = launch_status();
-  if (st != GPTQ_OK || !a.splits) return st;
-  // A row block with several units has more than the mean share of the work,
-  // so there are fewer than `target` of them (over all heads). Each gets a
-  // workgroup a row, or one for all where that would be very many.
-  const int64_t several = a.target / a.c.heads + 2, most = (several < blocks ? several : blocks) * a.c.heads;
-  const int rows = most * a.rows <= 4096 ? a.rows : 1;
-  hipLaunchKernelGGL(kv_join, dim3(unsigned(most * rows)), dim3(64 * ATT_WAVES), 0, s, a, rows);
   return launch_status();
 }
 template <int BITS, int DP>
-int launch_attend(AttArgs& a, int64_t blocks, bool split, hipStream_t s) {
+int launch_attend(const AttArgs& a, bool split, hipStream_t s) {
   if (a.c.dim == DP)
-    return split ? launch_attend<BITS, DP, true, true>(a, blocks, s) : launch_attend<BITS, DP, true, false>(a, blocks, s);
-  return split ? launch_attend<BITS, DP, false, true>(a, blocks, s) : launch_attend<BITS, DP, false, false>(a, blocks, s);
+    return split ? launch_attend<BITS, DP, true, true>(a, s) : launch_attend<BITS, DP, true, false>(a, s);
+  return split ? launch_attend<BITS, DP, false, true>(a, s) : launch_attend<BITS, DP, false, false>(a, s);
 }
 template <int BITS>
-int launch_attend(AttArgs& a, int64_t blocks, bool split, hipStream_t s) {
-  if (a.c.dim <= 64) return launch_attend<BITS, 64>(a, blocks, split, s);
-  if (a.c.dim <= 128) return launch_attend<BITS, 128>(a, blocks, split, s);
-  return launch_attend<BITS, 256>(a, blocks, split, s);
+int launch_attend(const AttArgs& a, bool split, hipStream_t s) {
+  if (a.c.dim <= 64) return launch_attend<BITS, 64>(a, split, s);
+  if (a.c.dim <= 128) return launch_attend<BITS, 128>(a, split, s);
+  return launch_attend<BITS, 256>(a, split, s);
 }
 
 }  // namespace
@@ -853,11 +528,9 @@ extern "C" size_t gptq_kv_attention_workspace_size(const gptq_kv_cache* cache, c
   KvCache c;
   KvBatch b;
   if (kv_views(cache, batch, &c, &b) != GPTQ_OK || q_heads < 1 || q_heads % c.heads != 0) return 0;
-  const int ratio = int(q_heads / c.heads);
   if (b.batch == 0 || b.n_tokens == 0) return 0;
-  const int64_t units = call_units(c, b, ratio, ATT_MAX_TARGET);
-  if (units <= call_blocks(b, ratio)) return 0;  // one unit each
-  return size_t(units) * size_t(c.heads) * size_t(call_rows(b, ratio)) * (size_t(c.dim) * sizeof(float) + sizeof(float2));
+  const Cut k = cut_call(c, b, int(q_heads / c.heads));
+  return size_t(k.parts) * size_t(c.heads) * size_t(k.rows) * (size_t(c.dim) * sizeof(float) + sizeof(float2));
 }
 
 extern "C" int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const void* q, int q_dtype,
@@ -877,10 +550,18 @@ extern "C" int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch
     return GPTQ_E_INVALID_ARG;
   if (a.b.n_tokens == 0 || a.b.batch == 0) return GPTQ_OK;
   a.ratio = int(q_heads / a.c.heads);
-  const int64_t blocks = call_blocks(a.b, a.ratio), units = call_units(a.c, a.b, a.ratio, ATT_MAX_TARGET);
-  a.rows = call_rows(a.b, a.ratio);
-  a.splits = units > blocks;
+  const Cut k = cut_call(a.c, a.b, a.ratio);
+  const bool split = q_dtype == GPTQ_F32 || out_dtype == GPTQ_F32;
+  // One round of resident workgroups is what the keys are split for.
+  const int dp = a.c.dim <= 64 ? 64 : a.c.dim <= 128 ? 128 : 256;
+  a.target = k.prompt ? prompt_target(dp, split) : 256 * att_waves_per_simd(cache->bits, dp, split);
+  const int64_t units = call_units(k, a.c.heads, a.target);
   if (units * a.c.heads >= (int64_t(1) << 24)) return GPTQ_E_INVALID_ARG;
+  a.block_rows = k.block_rows;
+  a.rows = k.rows;
+  a.splits = k.parts > 0;
+  a.units = int(units);
+  a.parts = int(k.parts);
   a.q = q;
   a.out = out;
   a.slopes = slopes;
@@ -891,13 +572,23 @@ extern "C" int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch
   a.q_dtype = q_dtype;
   a.out_dtype = out_dtype;
   a.q_vec = kv_vec16(q, ldq, q_dtype);
+  a.out_vec = kv_vec16(out, ldo, out_dtype);
   if (a.splits) {
     if (ws_bytes < gptq_kv_attention_workspace_size(cache, batch, q_heads)) return GPTQ_E_WORKSPACE;
     if (!ws || reinterpret_cast<uintptr_t>(ws) % 16 != 0) return GPTQ_E_INVALID_ARG;
     a.part_o = static_cast<float*>(ws);  // its rows stay 16-byte aligned: head_dim is a multiple of 16
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + units * a.c.heads * a.rows * a.c.dim);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + k.parts * a.c.heads * a.rows * a.c.dim);
   }
-  const bool split = q_dtype == GPTQ_F32 || out_dtype == GPTQ_F32;
   hipStream_t s = as_stream(stream);
-  return cache->bits == 4 ? launch_attend<4>(a, blocks, split, s) : launch_attend<8>(a, blocks, split, s);
+  st = k.prompt           ? launch_prompt(a, cache->bits, split, s)
+       : cache->bits == 4 ? launch_attend<4>(a, split, s)
+                          : launch_attend<8>(a, split, s);
+  if (st != GPTQ_OK || !a.splits) return st;
+  // A row block with several units has more than the mean share of the work,
+  // so there are fewer than `target` of them (over all heads). Each gets a
+  // workgroup a row, or one for all where that would be very many.
+  const int64_t several = a.target / a.c.heads + 2, most = (several < k.blocks ? several : k.blocks) * a.c.heads;
+  const int rows = most * a.rows <= 4096 ? a.rows : 1;
+  hipLaunchKernelGGL(kv_join, dim3(unsigned(most * rows)), dim3(64 * ATT_WAVES), 0, s, a, rows);
+  return launch_status();
 }

@@ -17,6 +17,7 @@
 // allocation of exactly its size.
 #include "../../post_weight_quantization_17_amd/csrc/kv_cache.hip"
 #include "../../post_weight_quantization_17_amd/csrc/kv_attention.hip"
+#include "../../post_weight_quantization_17_amd/csrc/kv_prompt.hip"
 
 #include <fstream>
 #include <string>

@@ -124,6 +124,18 @@ ATTEND = [
     (80, 4, 32, 2, 2, [61], [61], "f32", "f32", False, None),
     (256, 8, 32, 1, 2, [70], [17], "f16", "f16", False, None),
     (128, 8, 16, 1, 1, [40 + i for i in range(70)], [1 + i % 2 for i in range(70)], "f16", "f16", False, None),
+    # 64 query rows a sequence or more in the mean: the prompts' kernel
+    (128, 8, 16, 2, 2, [333], [333], "bf16", "bf16", False, None),
+    (64, 4, 64, 1, 4, [500, 0, 20], [133, 0, 20], "f16", "f16", True, None),
+    (64, 8, 16, 3, 3, [130], [129], "f32", "f32", False, None),
+    (256, 4, 32, 1, 2, [300], [70], "f16", "f16", False, None),
+    (256, 8, 16, 1, 1, [150, 40], [100, 40], "f32", "f16", False, None),
+    (80, 8, 128, 2, 6, [90, 200], [90, 1], "bf16", "f16", True, None),
+    (112, 4, 16, 1, 1, [257], [190], "f32", "f32", True, None),
+    (192, 8, 64, 1, 2, [66, 3], [66, 65], "f16", "bf16", False, None),
+    (16, 4, 16, 2, 64, [9], [2], "f16", "f32", False, None),
+    (48, 8, 64, 1, 5, [1500], [21], "bf16", "bf16", False, None),
+    (128, 4, 64, 1, 4, [3000, 100], [40, 5], "f16", "f16", False, None),
 ]
 
 

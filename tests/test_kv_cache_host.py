@@ -37,7 +37,8 @@ def kv_host(tmp_path_factory):
     if not os.path.exists(CLANG):
         pytest.skip("ROCm's clang++ is not installed")
     files = [os.path.join(HERE, "kv_main.cpp"), os.path.join(HERE, "kv", "hip", "hip_runtime.h"),
-             os.path.join(SRC, "kv_cache.hip"), os.path.join(SRC, "kv_attention.hip"), os.path.join(SRC, "kv_cache.h"),
+             os.path.join(SRC, "kv_cache.hip"), os.path.join(SRC, "kv_attention.hip"), os.path.join(SRC, "kv_prompt.hip"),
+             os.path.join(SRC, "kv_attention.h"), os.path.join(SRC, "kv_cache.h"),
              os.path.join(SRC, "gptq_common.h"), os.path.join(ROOT, "include", "gptq_mi355x.h")]
     h = hashlib.sha256(" ".join(FLAGS).encode())
     for f in files:
@@ -184,6 +185,14 @@ ATTEND = [
     (192, 4, 16, 1, 2, [30, 4], [3, 6], "bf16", "bf16", False, None),  # rows before the sequence's start
     (48, 8, 16, 1, 1, [600], [1], "f16", "f16", False, None),  # split over workgroups
     (128, 4, 128, 1, 4, [700, 290], [2, 1], "bf16", "f16", True, True),  # split, ragged
+    # the prompts' kernel: 64 query rows a sequence or more in the mean
+    (128, 4, 16, 1, 2, [75], [40], "f16", "f16", False, None),
+    (64, 8, 32, 1, 4, [50, 20], [33, 20], "bf16", "bf16", False, None),
+    (256, 4, 16, 1, 1, [70], [66], "f16", "f16", False, None),
+    (80, 8, 16, 1, 4, [60, 0, 35], [50, 0, 24], "f32", "f32", True, None),
+    (16, 4, 16, 2, 64, [9], [2], "f16", "f32", False, None),
+    (48, 8, 64, 1, 1, [600], [70], "bf16", "f16", False, None),  # split over workgroups
+    (192, 8, 16, 1, 1, [66, 3], [66, 65], "f16", "bf16", False, None),  # rows before the sequence's start
 ]
 
 
@@ -246,9 +255,12 @@ def test_broken_tables_lengths_and_starts_stay_in_bounds(kv_host, name):
         got = rd("k_out", np.float16, want[0].shape).astype(np.float64)
         assert np.all(np.abs(got - want[0]) <= np.abs(want[0]) * 2.0**-10.99 + 2.0**-25)
         assert int(rd("info", np.int32)[0]) == int(bad)
-    qf, qs = C.cast(rng.standard_normal((4, 4, 64)), "f16")
-    rd = run(kv_host, "ba" + name, "attend", cache, table, lens, starts, 4, ld=256, ld_out=256, q_heads=4, scale=0.125, q=qs)
-    if ordered:
+    for hq in (4, 66):  # 66: the prompts' kernel
+        qf, qs = C.cast(rng.standard_normal((4, hq, 64)), "f16")
+        rd = run(kv_host, f"ba{hq}{name}", "attend", cache, table, lens, starts, 4, ld=hq * 64, ld_out=hq * 64, q_heads=hq,
+                 scale=0.125, q=qs)
+        if not ordered:
+            continue
         if lens.max() < 10**5:
             want, mag, _, bad = K.attention(qf, cache, table, lens, starts, 0.125)
             got = rd("out", np.float16, want.shape).astype(np.float64)
