@@ -609,7 +609,7 @@ def _kv_rows(name: str, t: torch.Tensor, n: int, heads: int, dim: int, index: in
 
 def _kv_call(index: int, fn, *args) -> int:
     """Calls fn(*args, stream) on device ``index`` and its current stream."""
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         return fn(*args, torch._C._cuda_getCurrentRawStream(index))
     with torch.cuda.device(index):
         return fn(*args, torch._C._cuda_getCurrentRawStream(index))

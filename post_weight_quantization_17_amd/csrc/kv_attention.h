@@ -13,7 +13,7 @@ constexpr int ATT_ROWS = 16;                     // query rows of a wave's MFMA
 constexpr int ATT_TILE = 32;                     // keys a wave takes at a time
 constexpr int ATT_MIN_CHUNK = 256;               // fewest keys of a workgroup when a row's keys are split
 constexpr int ATT_MAX_TARGET = 4 * 256;          // most workgroups that the keys are split for (Seq)
-constexpr int PROMPT_MAX_TARGET = 3 * 256;       // and in the prompts' kernel
+constexpr int PROMPT_MAX_TARGET = 2 * 256;       // and in the prompts' kernel
 constexpr int64_t PROMPT_ROWS = 64;               // see cut_call
 constexpr float ATT_W_TOP = 8.0f;                // log2 of the largest weight after a rescaling
 constexpr float ATT_W_LIMIT = 32768.0f;          // a weight above this asks for the next one

@@ -74,8 +74,28 @@ kv_attend(AttArgs a) {
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int g = lane / 16, n16 = lane % 16;
   const int kv = int(blockIdx.x % unsigned(c.heads));
-  const Seq sq = find_unit<false>(a, int(blockIdx.x / unsigned(c.heads)), lane);
-  if (sq.b < 0) return;  // whole workgroup; uniform
+  // A tile's pages are the table entries of its two 16-key subtiles.
+  struct Ids {
+    int id[2];
+  };
+  Ids ids{{-1, -1}};
+  Seq sq;
+  const bool plain = !a.splits && !a.b.starts;  // one unit a row block, one token a sequence
+  if (plain) {
+    // The first tile's pages are known without the length: both loads at once.
+    const int at = int(blockIdx.x / unsigned(c.heads)), per = int(row_blocks(1, a.ratio, a.block_rows));
+    sq = Seq{at / per, at / per, 1, at % per, 0, 1, 0, 0, 0xFFFFFF80u};
+    const int len_now = a.b.lens[sq.b];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int page = (wave * ATT_TILE + 16 * u) >> c.shift;
+      if (page < a.b.max_pages) ids.id[u] = a.b.table[sq.b * a.b.ld + page];
+    }
+    sq.len = __builtin_amdgcn_readfirstlane(len_now);
+  } else {
+    sq = find_unit<false>(a, int(blockIdx.x / unsigned(c.heads)), lane);
+    if (sq.b < 0) return;  // whole workgroup; uniform
+  }
 
   const int64_t cap = a.b.max_pages << c.shift;
   const int64_t len = sq.len;
@@ -104,9 +124,6 @@ kv_attend(AttArgs a) {
   constexpr uint32_t step = ATT_WAVES * ATT_TILE;
   const int words = FULL ? DP * BITS / 32 : c.words;
   const int32_t* const pages = a.b.table + sq.b * a.b.ld;
-  struct Ids {
-    int id[2];
-  };
   const auto look_up = [&](uint32_t p0) {
     Ids r{{-1, -1}};
 #pragma unroll
@@ -177,7 +194,7 @@ kv_attend(AttArgs a) {
 
   uint32_t p0 = k0 + wave * ATT_TILE;
   Rows at = {};
-  Ids ids = look_up(p0);
+  if (!plain) ids = look_up(p0);
   if (p0 < k1) {
     at = locate(p0, ids);
     load_keys(at);
@@ -586,9 +603,9 @@ extern "C" int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch
   if (st != GPTQ_OK || !a.splits) return st;
   // A row block with several units has more than the mean share of the work,
   // so there are fewer than `target` of them (over all heads). Each gets a
-  // workgroup a row, or one for all where that would be very many.
+  // workgroup a row, or fewer where that would be very many.
   const int64_t several = a.target / a.c.heads + 2, most = (several < k.blocks ? several : k.blocks) * a.c.heads;
-  const int rows = most * a.rows <= 4096 ? a.rows : 1;
+  const int rows = most * a.rows <= 4096 ? a.rows : int((4096 + most - 1) / most);
   hipLaunchKernelGGL(kv_join, dim3(unsigned(most * rows)), dim3(64 * ATT_WAVES), 0, s, a, rows);
   return launch_status();
 }

@@ -5,7 +5,7 @@
 // There each wave converts the codes it multiplies with, which is free while
 // the cache's bytes bound the call, but with many rows the same keys would be
 // converted again for every 16 of them. Here a workgroup's 4 waves take RT
-// 16-row tiles each over the same keys: 32 keys at a time are converted once,
+// 16-row tiles each over the same keys: 64 keys at a time are converted once,
 // a quarter by each wave, and left in LDS as MFMA operands (fragments of 16
 // bytes a lane, read back by lane, without bank conflicts) in two buffers: a
 // barrier a tile. The codes' zeros are subtracted during the conversion, so
@@ -17,13 +17,15 @@ namespace gptq {
 namespace {
 
 constexpr int prompt_tiles(int dp) { return dp <= 128 ? 2 : 1; }
-constexpr int prompt_waves_per_simd(int dp, bool split) { return dp == 64 ? (split ? 2 : 3) : dp == 128 && !split ? 2 : 1; }
+constexpr int prompt_waves_per_simd(int dp, bool split) { return dp == 64 || (dp == 128 && !split) ? 2 : 1; }
+
+constexpr int ROWS_TILE = 64;  // keys at a time
 
 template <int DP>
 struct Stage {
-  half8 k[2][DP / 32][64];  // [16-key half][32 d][lane]
-  half8 v[DP / 16][64];     // [d within a lane's share][lane]
-  float sk[32], sv[32];     // scales of the keys
+  half8 k[4][DP / 32][64];  // [16 keys][32 d][lane]
+  half8 v[2][DP / 16][64];  // [32 keys][d within a lane's share][lane]
+  float sk[64], sv[64];     // scales of the keys
 };
 
 template <int BITS, int DP, bool FULL, bool SPLIT>
@@ -81,33 +83,33 @@ kv_attend_rows(AttArgs a) {
     q[t].load(a, r.live, r.token, r.head, g);
   }
 
-  // Conversion: waves 0 and 1 the keys' 16-key halves, waves 2 and 3 the
-  // lower and upper half of each lane's d of the values.
+  // Conversion: each wave takes 16 of the keys, and of the values the 32 keys
+  // `span` and the lower or upper half of each lane's d.
   const int words = FULL ? DP * BITS / 32 : c.words;
   const int32_t* const pages = a.b.table + sq.b * a.b.ld;
-  const int part = wave & 1;
+  const int part = wave & 1, span = wave >> 1;
   struct Raw {
-    uint32_t w[KW > 8 * VW ? KW : 8 * VW];
-    uint32_t kg, vg;  // waves 0, 1: of key n16 of the half
-    uint4 zg[2];      // waves 2, 3: grids of this lane's 8 keys
-    uint32_t ok;      // bit u: half u lies on a page
+    uint32_t k[KW], v[8 * VW];
+    uint32_t kg, vg;  // grids of key n16 of the wave's 16
+    uint4 zg[2];      // grids of the 8 keys of the values
+    uint32_t ok;      // bit u: the 16 keys u lie on a page
   };
   struct Ids {
-    int id[2];
+    int id[4];
   };
   const auto look_up = [&](uint32_t p0) {
-    Ids r{{-1, -1}};
+    Ids r{{-1, -1, -1, -1}};
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 4; ++u)
       if (p0 + 16 * u < k1) r.id[u] = pages[(p0 + 16 * u) >> c.shift];
     return r;
   };
   const int vc = n16 * DPL < c.dim ? n16 : 0;  // lanes past the head's end repeat the first one's codes
   const auto fetch = [&](uint32_t p0, const Ids& ids, Raw& raw) {
-    int64_t at[2];
+    int64_t at[4];
     raw.ok = 0;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < 4; ++u) {
       const uint32_t p = p0 + 16 * u;
       int64_t id = __builtin_amdgcn_readfirstlane(ids.id[u]);
       if (id >= 0 && id < c.n_pages) {
@@ -118,37 +120,35 @@ kv_attend_rows(AttArgs a) {
       }
       at[u] = ((id * c.heads + kv) << c.shift) + (p & ((1u << c.shift) - 1));
     }
-    if (wave < 2) {
-      const int64_t mine = part ? at[1] : at[0];
-      const char* kr = reinterpret_cast<const char*>(c.k_codes + mine * words);
-      raw.kg = c.k_grid[mine + n16];
-      raw.vg = c.v_grid[mine + n16];
-      if constexpr (FULL) {
-        load_words<KW>(kr + 4u * (n16 * words + g * KW), raw.w);
-      } else {
-        constexpr int W = BITS / 4;  // words of a block of 8 d
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          const int b = lane_block<DP, FULL>(g, j);
-          load_words<W>(kr + 4u * (n16 * words + W * (8 * b < c.dim ? b : 0)), &raw.w[W * j]);
-        }
-      }
+    const int64_t mine = wave == 0 ? at[0] : wave == 1 ? at[1] : wave == 2 ? at[2] : at[3];
+    const char* kr = reinterpret_cast<const char*>(c.k_codes + mine * words);
+    raw.kg = c.k_grid[mine + n16];
+    raw.vg = c.v_grid[mine + n16];
+    if constexpr (FULL) {
+      load_words<KW>(kr + 4u * (n16 * words + g * KW), raw.k);
     } else {
+      constexpr int W = BITS / 4;  // words of a block of 8 d
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        raw.zg[u] = *reinterpret_cast<const uint4*>(c.v_grid + at[u] + 4 * g);
-        const char* vr = reinterpret_cast<const char*>(c.v_codes + (at[u] + 4 * g) * words) + DPL * BITS / 8 * vc + HB / 8 * part;
+      for (int j = 0; j < NJ; ++j) {
+        const int b = lane_block<DP, FULL>(g, j);
+        load_words<W>(kr + 4u * (n16 * words + W * (8 * b < c.dim ? b : 0)), &raw.k[W * j]);
+      }
+    }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const char* vp = vr + 4 * r * words;
-          uint32_t* w = &raw.w[(4 * u + r) * VW];
-          if constexpr (HB == 8)
-            w[0] = *reinterpret_cast<const uint8_t*>(vp);
-          else if constexpr (HB == 16)
-            w[0] = *reinterpret_cast<const uint16_t*>(vp);
-          else
-            load_words<VW>(vp, w);
-        }
+    for (int u = 0; u < 2; ++u) {
+      const int64_t base = (span ? at[2 + u] : at[u]) + 4 * g;
+      raw.zg[u] = *reinterpret_cast<const uint4*>(c.v_grid + base);
+      const char* vr = reinterpret_cast<const char*>(c.v_codes + base * words) + DPL * BITS / 8 * vc + HB / 8 * part;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const char* vp = vr + 4 * r * words;
+        uint32_t* w = &raw.v[(4 * u + r) * VW];
+        if constexpr (HB == 8)
+          w[0] = *reinterpret_cast<const uint8_t*>(vp);
+        else if constexpr (HB == 16)
+          w[0] = *reinterpret_cast<const uint16_t*>(vp);
+        else
+          load_words<VW>(vp, w);
       }
     }
   };
@@ -160,51 +160,47 @@ kv_attend_rows(AttArgs a) {
     return as_half8(s[0], s[1], s[2], s[3]);
   };
   const auto convert = [&](const Raw& raw, Stage<DP>& st) {
-    if (wave < 2) {
-      const uint32_t z1 = MAGIC + (kv_zero<BITS>(raw.kg) * 0x10001u << AT);
-      const uint32_t z[4] = {z1, z1, z1, z1};
+    uint32_t h[4], z[4], two[4];
+    const uint32_t z1 = MAGIC + (kv_zero<BITS>(raw.kg) * 0x10001u << AT);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        uint32_t h[4];
-        key_codes<BITS>(&raw.w[j * (BITS / 4)], h, kc);
-        st.k[part][j][lane] = minus(h, z);
-      }
-      if (g == 0) {
-        st.sk[16 * part + n16] = kv_scale(raw.kg);
-        st.sv[16 * part + n16] = kv_scale(raw.vg);
-      }
-    } else {
-      uint32_t z[4];
+    for (int e = 0; e < 4; ++e) z[e] = z1;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint4 w = raw.zg[e / 2];
-        const uint32_t z0 = kv_zero<BITS>(e % 2 ? w.z : w.x), z1 = kv_zero<BITS>(e % 2 ? w.w : w.y);
-        z[e] = (z0 | z1 << 16) << AT | MAGIC;
-      }
-      half8* out = &st.v[part * (DPL / 2)][lane];  // [m][lane] from this wave's first m on
-      uint32_t h[4], two[4];
+    for (int j = 0; j < NJ; ++j) {
+      key_codes<BITS>(&raw.k[j * (BITS / 4)], h, kc);
+      st.k[wave][j][lane] = minus(h, z);
+    }
+    if (g == 0) {
+      st.sk[16 * wave + n16] = kv_scale(raw.kg);
+      st.sv[16 * wave + n16] = kv_scale(raw.vg);
+    }
 #pragma unroll
-      for (int vw = 0; vw < VW; ++vw) {
+    for (int e = 0; e < 4; ++e) {
+      const uint4 w = raw.zg[e / 2];
+      const uint32_t z0 = kv_zero<BITS>(e % 2 ? w.z : w.x), z2 = kv_zero<BITS>(e % 2 ? w.w : w.y);
+      z[e] = (z0 | z2 << 16) << AT | MAGIC;
+    }
+    half8* out = &st.v[span][part * (DPL / 2)][lane];  // [m][lane] from this wave's first m on
 #pragma unroll
-        for (int hi = 0; hi < (HB >= 32 ? 2 : 1); ++hi) {
-          // 16 bits of this word of the keys of a pair, side by side
+    for (int vw = 0; vw < VW; ++vw) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            two[e] = __builtin_amdgcn_perm(raw.w[(2 * e + 1) * VW + vw], raw.w[2 * e * VW + vw], hi ? 0x07060302u : 0x05040100u);
-          constexpr int PER = 16 / BITS < DPL / 2 ? 16 / BITS : DPL / 2;  // d in them
-          half8* o = out + 64 * ((2 * vw + hi) * (16 / BITS));
+      for (int hi = 0; hi < (HB >= 32 ? 2 : 1); ++hi) {
+        // 16 bits of this word of the keys of a pair, side by side
 #pragma unroll
-          for (int m = 0; m < PER; ++m) {
+        for (int e = 0; e < 4; ++e)
+          two[e] = __builtin_amdgcn_perm(raw.v[(2 * e + 1) * VW + vw], raw.v[2 * e * VW + vw], hi ? 0x07060302u : 0x05040100u);
+        constexpr int PER = 16 / BITS < DPL / 2 ? 16 / BITS : DPL / 2;  // d in them
+        half8* o = out + 64 * ((2 * vw + hi) * (16 / BITS));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if constexpr (BITS == 4)
-                h[e] = m == 0 ? nibbles<0>(two[e], kc) : m == 1 ? nibbles<1>(two[e], kc) : m == 2 ? nibbles<2>(two[e], kc)
-                                                                                                   : nibbles<3>(two[e], kc);
-              else
-                h[e] = m == 0 ? byte_pair<0, 2>(two[e], kc) : byte_pair<1, 3>(two[e], kc);
-            }
-            o[64 * m] = minus(h, z);
+        for (int m = 0; m < PER; ++m) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (BITS == 4)
+              h[e] = m == 0 ? nibbles<0>(two[e], kc) : m == 1 ? nibbles<1>(two[e], kc) : m == 2 ? nibbles<2>(two[e], kc)
+                                                                                                 : nibbles<3>(two[e], kc);
+            else
+              h[e] = m == 0 ? byte_pair<0, 2>(two[e], kc) : byte_pair<1, 3>(two[e], kc);
           }
+          o[64 * m] = minus(h, z);
         }
       }
     }
@@ -220,7 +216,8 @@ kv_attend_rows(AttArgs a) {
     for (int m = 0; m < DPL; ++m) o[t][m] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  const auto compute = [&](uint32_t p0, uint32_t ok, const Stage<DP>& st) {
+  // 32 of the tile's keys (half h) from p0 on; ok: bit u for its 16 keys u.
+  const auto compute = [&](uint32_t p0, uint32_t ok, const Stage<DP>& st, int half) {
     floatx4 acc[RT][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -228,7 +225,7 @@ kv_attend_rows(AttArgs a) {
       for (int t = 0; t < RT; ++t) acc[t][u] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const half8 keys = st.k[u][j][lane];
+        const half8 keys = st.k[2 * half + u][j][lane];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
           if constexpr (SPLIT) acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(keys, q[t].l[j], acc[t][u], 0, 0, 0);
@@ -236,30 +233,25 @@ kv_attend_rows(AttArgs a) {
         }
       }
     }
-    float sk[8], sv[8];
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        sk[4 * u + r] = st.sk[16 * u + 4 * g + r];
-        sv[4 * u + r] = st.sv[16 * u + 4 * g + r];
-      }
     half8 wh[RT], wl[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       const Row& r = row[t];
       float x[8], s[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] = acc[t][e / 4][e % 4] * (sk[e] * q[t].scale);
-        s[e] = sv[e];
+      for (int u = 0; u < 2; ++u) {
+        const float4 sk = *reinterpret_cast<const float4*>(&st.sk[32 * half + 16 * u + 4 * g]);
+        const float4 sv = *reinterpret_cast<const float4*>(&st.sv[32 * half + 16 * u + 4 * g]);
+        x[4 * u] = acc[t][u][0] * (sk.x * q[t].scale), x[4 * u + 1] = acc[t][u][1] * (sk.y * q[t].scale);
+        x[4 * u + 2] = acc[t][u][2] * (sk.z * q[t].scale), x[4 * u + 3] = acc[t][u][3] * (sk.w * q[t].scale);
+        s[4 * u] = sv.x, s[4 * u + 1] = sv.y, s[4 * u + 2] = sv.z, s[4 * u + 3] = sv.w;
       }
       if (a.slopes) {
         const float rel = float(int(p0) + 4 * g - r.pos);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = fmaf(r.slope, rel + float(16 * (e / 4) + e % 4), x[e]);
       }
-      if (p0 + ATT_TILE > r.all || ok != 3u) {
+      if (p0 + 32 > r.all || ok != 3u) {
         const int left = int(r.lim) - int(p0) - 4 * g;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -293,16 +285,18 @@ kv_attend_rows(AttArgs a) {
           w[e] = p[e] * s[e];
         }
       }
+      float sum = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        l[t] += p[e];
+        sum += p[e];
         wh[t][e] = _Float16(w[e]);
         if constexpr (SPLIT) wl[t][e] = _Float16(w[e] - float(wh[t][e]));
       }
+      l[t] += sum;
     }
 #pragma unroll
     for (int m = 0; m < DPL; ++m) {
-      const half8 values = st.v[m][lane];
+      const half8 values = st.v[half][m][lane];
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         if constexpr (SPLIT) o[t][m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(values, wl[t], o[t][m], 0, 0, 0);
@@ -318,26 +312,28 @@ kv_attend_rows(AttArgs a) {
     Raw raw;
     Ids ids = look_up(k0);
     fetch(k0, ids, raw);
-    ids = look_up(k0 + ATT_TILE);
+    ids = look_up(k0 + ROWS_TILE);
     uint32_t ok = raw.ok;
     convert(raw, stage[0]);
-    if (k0 + ATT_TILE < k1) {
-      fetch(k0 + ATT_TILE, ids, raw);
-      ids = look_up(k0 + 2 * ATT_TILE);
+    if (k0 + ROWS_TILE < k1) {
+      fetch(k0 + ROWS_TILE, ids, raw);
+      ids = look_up(k0 + 2 * ROWS_TILE);
     }
     __syncthreads();
     int b = 0;
-    for (uint32_t p0 = k0; p0 < k1; p0 += ATT_TILE, b ^= 1) {
+    for (uint32_t p0 = k0; p0 < k1; p0 += ROWS_TILE, b ^= 1) {
       uint32_t next_ok = 0;
-      if (p0 + ATT_TILE < k1) {
+      if (p0 + ROWS_TILE < k1) {
         next_ok = raw.ok;
         convert(raw, stage[b ^ 1]);
-        if (p0 + 2 * ATT_TILE < k1) {
-          fetch(p0 + 2 * ATT_TILE, ids, raw);
-          ids = look_up(p0 + 3 * ATT_TILE);
+        if (p0 + 2 * ROWS_TILE < k1) {
+          fetch(p0 + 2 * ROWS_TILE, ids, raw);
+          ids = look_up(p0 + 3 * ROWS_TILE);
         }
       }
-      if (p0 < any) compute(p0, ok, stage[b]);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h)
+        if (p0 + 32 * h < any) compute(p0 + 32 * h, ok >> (2 * h) & 3u, stage[b], h);
       ok = next_ok;
       __syncthreads();
     }
