@@ -340,9 +340,9 @@ struct Query {
   }
 };
 
-// The prompts' kernel (kv_prompt.hip): 128-row blocks, 64 for heads wider than 128.
-constexpr int prompt_rows(int dim) { return dim <= 128 ? 128 : 64; }
-int prompt_target(int dim, bool split);
+// The prompts' kernel (kv_prompt.hip).
+constexpr int PROMPT_BLOCK = 128;  // query rows of its row blocks
+int prompt_target(int dp, bool split);
 int launch_prompt(const AttArgs& a, int bits, bool split, hipStream_t s);
 
 }  // namespace gptq

@@ -155,11 +155,17 @@ kv_attend(AttArgs a) {
     return r;
   };
   const int vc = n16 * DPL < c.dim ? n16 : 0;  // lanes past the head's end repeat the first one's codes
-  const uint32_t k_off = FULL ? 4u * (n16 * words + g * KW) : 4u * n16 * words;
-  const uint32_t v_off = DPL * BITS == 16 ? 16u * g * words + 2u * vc : 16u * g * words + 4u * VW * vc;
+  uint32_t k_off = FULL ? 4u * (n16 * words + g * KW) : 4u * n16 * words;
+  uint32_t key_off = 4u * n16, quad_off = 16u * g;  // of grid words
+  uint32_t v_off = DPL * BITS == 16 ? 16u * g * words + 2u * vc : 16u * g * words + 4u * VW * vc;
   const auto blk = [&](int j) { return lane_block<DP, FULL>(g, j); };
   TL t;
+  // Base pointers are uniform, offsets 32 bits a lane; their sums are formed by
+  // the loads.
   const auto load_keys = [&](const Rows& at) {
+    KV_FRESH_V(k_off);
+    KV_FRESH_V(key_off);
+    KV_FRESH_V(quad_off);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const char* kr = reinterpret_cast<const char*>(c.k_codes + at.at[u] * words);
@@ -172,14 +178,16 @@ kv_attend(AttArgs a) {
         for (int j = 0; j < NJ; ++j)
           load_words<W>(kr + (k_off + 4u * W * (8 * blk(j) < c.dim ? blk(j) : 0)), &t.k[u][W * j]);
       }
-      t.kg[u] = *reinterpret_cast<const uint4*>(gr + 16u * g);
-      if constexpr (SPLIT) t.kz[u] = *reinterpret_cast<const uint32_t*>(gr + 4u * n16);
+      t.kg[u] = *reinterpret_cast<const uint4*>(gr + quad_off);
+      if constexpr (SPLIT) t.kz[u] = *reinterpret_cast<const uint32_t*>(gr + key_off);
     }
   };
   const auto load_values = [&](const Rows& at) {
+    KV_FRESH_V(v_off);
+    KV_FRESH_V(quad_off);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      t.vg[u] = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(c.v_grid + at.at[u]) + 16u * g);
+      t.vg[u] = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(c.v_grid + at.at[u]) + quad_off);
       const char* vr = reinterpret_cast<const char*>(c.v_codes + at.at[u] * words);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -259,11 +267,12 @@ kv_attend(AttArgs a) {
         sv[e] = seen ? sv[e] : 0.0f;
       }
     }
-    float p[8], w[8], big = 0.0f;
+    float w[8], sum = 0.0f, big = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      p[e] = __builtin_amdgcn_exp2f(x[e] - M);
-      w[e] = p[e] * sv[e];
+      const float p = __builtin_amdgcn_exp2f(x[e] - M);
+      sum += p;
+      w[e] = p * sv[e];
       big = fmaxf(big, w[e]);
     }
     if (__any(big > ATT_W_LIMIT)) {
@@ -278,16 +287,18 @@ kv_attend(AttArgs a) {
       l *= f;
 #pragma unroll
       for (int m = 0; m < DPL; ++m) o[m] *= f;
+      sum = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        p[e] = __builtin_amdgcn_exp2f(x[e] - M);
-        w[e] = p[e] * sv[e];
+        const float p = __builtin_amdgcn_exp2f(x[e] - M);
+        sum += p;
+        w[e] = p * sv[e];
       }
     }
+    l += sum;
     half8 wh, wl;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      l += p[e];
       wh[e] = _Float16(w[e]);
       if constexpr (SPLIT) wl[e] = _Float16(w[e] - float(wh[e]));
     }
@@ -487,6 +498,8 @@ kv_join(AttArgs a, int rows) {
   }
 }
 
+constexpr int64_t JOIN_GROUPS = 1024;  // workgroups of a join, or one a row block if those are more
+
 // How a call is cut: everything that does not depend on device data, nor on
 // the types (workspace sizes are asked for without them).
 struct Cut {
@@ -499,10 +512,10 @@ struct Cut {
 };
 Cut cut_call(const KvCache& c, const KvBatch& b, int ratio) {
   Cut k;
-  // The prompts' kernel converts the cache once for 4 waves of rows; it takes
+  // The prompts' kernel converts the cache once for 8 waves of rows; it takes
   // the calls whose sequences have PROMPT_ROWS query rows in the mean.
   k.prompt = b.starts && b.n_tokens * ratio >= PROMPT_ROWS * b.batch;
-  k.block_rows = k.prompt ? prompt_rows(c.dim) : ATT_ROWS;
+  k.block_rows = k.prompt ? PROMPT_BLOCK : ATT_ROWS;
   k.rows = b.starts || ratio > k.block_rows ? k.block_rows : ratio;
   k.blocks = b.starts ? row_blocks(b.n_tokens, ratio, k.block_rows) + b.batch : b.batch * row_blocks(1, ratio, k.block_rows);
   k.chunks = ((b.max_pages << c.shift) + ATT_MIN_CHUNK - 1) / ATT_MIN_CHUNK;
@@ -605,7 +618,7 @@ extern "C" int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch
   // so there are fewer than `target` of them (over all heads). Each gets a
   // workgroup a row, or fewer where that would be very many.
   const int64_t several = a.target / a.c.heads + 2, most = (several < k.blocks ? several : k.blocks) * a.c.heads;
-  const int rows = most * a.rows <= 4096 ? a.rows : int((4096 + most - 1) / most);
+  const int rows = most * a.rows <= JOIN_GROUPS ? a.rows : int((JOIN_GROUPS + most - 1) / most);
   hipLaunchKernelGGL(kv_join, dim3(unsigned(most * rows)), dim3(64 * ATT_WAVES), 0, s, a, rows);
   return launch_status();
 }

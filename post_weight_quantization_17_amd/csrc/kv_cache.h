@@ -9,9 +9,12 @@ namespace gptq {
 
 // Keeps the compiler from seeing a constant, so that it stays in an SGPR or
 // a VGPR instead of becoming a literal of every instruction that uses it.
+// KV_FRESH_V makes a value new at every pass, so that nothing formed with it
+// (an address, say) is carried through a loop.
 #ifndef KV_OPAQUE_S
 #define KV_OPAQUE_S(x) asm("" : "+s"(x))
 #define KV_OPAQUE_V(x) asm("" : "+v"(x))
+#define KV_FRESH_V(x) asm volatile("" : "+v"(x))
 #endif
 
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));

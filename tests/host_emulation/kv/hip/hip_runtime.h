@@ -30,6 +30,7 @@
 #define __shared__ static
 #define KV_OPAQUE_S(x) ((void)(x))
 #define KV_OPAQUE_V(x) ((void)(x))
+#define KV_FRESH_V(x) ((void)(x))
 
 struct dim3 {
   uint32_t x, y, z;
