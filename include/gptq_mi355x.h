@@ -372,7 +372,7 @@ int gptq_dequant_matvec(const uint32_t* packed, const float* scales, const int32
  * the last ones of their sequences:
  *   table    int32 [batch] rows ld_table apart: entry i of a row is the page
  *            of positions i * page_size and on; max_pages entries a row.
- *            Entries past a sequence's length are not read.
+ *            Entries past a sequence's length are not used.
  *   lens     int32 [batch]: tokens of each sequence, with those of the call.
  *   starts   int32 [batch + 1], not decreasing: the call's rows starts[b] ..
  *            starts[b + 1] - 1 are the last tokens of sequence b; NULL: one

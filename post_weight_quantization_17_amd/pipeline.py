@@ -3,7 +3,8 @@
 xuzou.cn reading card of the GPTQ paper, section 计算设置: the model is
 quantized one block at a time; calibration data run through a block give
 each layer's Hessian, the layers are quantized, and the quantized block is
-run to produce the next block's inputs. Two pieces of that:
+run to produce the next block's inputs. Two pieces of that, and the use of
+their result:
 
 * ``quantize_shared_input``: layers that read the same input (the q/k/v
   projections) share one Hessian, accumulated over the calibration chunks
@@ -11,6 +12,9 @@ run to produce the next block's inputs. Two pieces of that:
   each layer's loss is the library's own fp64 sum.
 * ``quantize_mlp_block``: up layer, ReLU, down layer, quantized in order,
   the down layer calibrated on the output of the quantized up layer.
+* ``attention_block``: tokens through packed q/k/v projections, the quantised
+  key-value cache and the packed output projection, for prompts and for
+  single tokens.
 
 Every step runs in the library's kernels, the quantized layers included
 (``gptq_dequant_gemm``: tokens x packed weights on the fp16 MFMA with the
@@ -21,14 +25,18 @@ workspaces and streams.
 
 from __future__ import annotations
 
-from typing import Iterable, List, Sequence
+from typing import Iterable, List, Optional, Sequence
 
 import torch
 
 from . import (
+    KVCache,
     Quantized,
     gptq_dequant_gemm,
+    gptq_dequant_matvec,
     gptq_hessian_accumulate,
+    gptq_kv_attention,
+    gptq_kv_cache_write,
     gptq_prepare_hinv,
     gptq_quantize_layer,
 )
@@ -68,3 +76,26 @@ def quantize_mlp_block(X0: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tenso
     q_down = gptq_quantize_layer(W_down, hv_down.U, bits, group_size, block)
     X2 = gptq_dequant_gemm(q_down.packed, q_down.scales, q_down.zeros, d_ff, bits, group_size, X1)
     return dict(H_up=H_up, hinv_up=hv_up, up=q_up, X1=X1, H_down=H_down, hinv_down=hv_down, down=q_down, X2=X2)
+
+
+def attention_block(x: torch.Tensor, q: Quantized, k: Quantized, v: Quantized, o: Quantized, bits: int, group_size: int,
+                    cache: KVCache, table: torch.Tensor, lens: torch.Tensor, starts: Optional[torch.Tensor] = None,
+                    slopes: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Tokens x [n_tokens, d] (fp16) through an attention sub-block: the
+    packed projections q [q_heads * head_dim, d], k and v [kv_heads *
+    head_dim, d]; k and v stored in ``cache``; causal attention over it; the
+    packed output projection o [d, q_heads * head_dim].
+
+    ``table``, ``lens`` and ``starts`` as in gptq_kv_cache_write (``lens``
+    counts these tokens). Without ``starts`` (one token a sequence) the
+    projections are matrix-vector products and the result is fp32; with it
+    they run as gptq_dequant_gemm and the result is fp16. ``slopes``: linear
+    position biases. Rows past ``starts[batch]`` are unspecified."""
+    dim = cache.head_dim
+    project = gptq_dequant_matvec if starts is None else gptq_dequant_gemm
+    with torch.cuda.device(x.device):
+        heads = [project(p.packed, p.scales, p.zeros, x.shape[1], bits, group_size, x).unflatten(1, (-1, dim))
+                 for p in (q, k, v)]
+        gptq_kv_cache_write(cache, heads[1], heads[2], table, lens, starts=starts)
+        a = gptq_kv_attention(heads[0], cache, table, lens, starts=starts, slopes=slopes, dtype=torch.float16).flatten(1)
+        return project(o.packed, o.scales, o.zeros, a.shape[1], bits, group_size, a)
