@@ -553,36 +553,32 @@ def gptq_kv_cache_alloc(n_pages: int, page_size: int, kv_heads: int, head_dim: i
                    v_grid=z(*rows), head_dim=head_dim, bits=bits, info=z(1))
 
 
-def _kv_ints(name: str, t: torch.Tensor, index: int) -> None:
-    # get_device() is -1 for a CPU tensor
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on the cache's GPU")
-    if t.dtype != torch.int32:
-        raise ValueError(f"{name} must be int32")
-
-
 def _kv_batch(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, starts: Optional[torch.Tensor], n_tokens: int):
     """The batch struct of a call, after the checks of shapes and devices."""
     index = cache._index
-    _kv_ints("table", table, index)
-    _kv_ints("lens", lens, index)
+    if table.get_device() != index or table.dtype != torch.int32:
+        raise ValueError("table must be int32 and on the cache's GPU")
+    if lens.get_device() != index or lens.dtype != torch.int32:
+        raise ValueError("lens must be int32 and on the cache's GPU")
     if lens.dim() != 1 or not lens.is_contiguous():
         raise ValueError("lens must be a contiguous vector")
     batch = lens.shape[0]
-    if table.dim() != 2 or table.shape[0] != batch or (table.shape[1] > 1 and table.stride(1) != 1):
+    if table.dim() != 2:
+        raise ValueError("table must be [batch, max_pages]")
+    (rows, width), (ld, step) = table.shape, table.stride()
+    if rows != batch or (width > 1 and step != 1):
         raise ValueError("table must be [batch, max_pages] with unit column stride")
     if starts is None:
         if n_tokens != batch:
             raise ValueError("without starts there is one token a sequence")
         sp = None
     else:
-        _kv_ints("starts", starts, index)
+        if starts.get_device() != index or starts.dtype != torch.int32:
+            raise ValueError("starts must be int32 and on the cache's GPU")
         if starts.shape != (batch + 1,) or not starts.is_contiguous():
             raise ValueError("starts must be a contiguous [batch + 1] vector")
         sp = starts.data_ptr()
-    width = table.shape[1]
-    return _KvBatchStruct(table.data_ptr(), table.stride(0) if batch > 1 else width, width, lens.data_ptr(), sp, batch,
-                          n_tokens)
+    return _KvBatchStruct(table.data_ptr(), ld if batch > 1 else width, width, lens.data_ptr(), sp, batch, n_tokens)
 
 
 _KV_DTYPES = {torch.float16: GPTQ_F16, torch.float32: GPTQ_F32, torch.bfloat16: GPTQ_BF16}
@@ -649,7 +645,7 @@ def gptq_kv_cache_read(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, 
             n_tokens = lens.shape[0]
         shape = (n_tokens, cache._heads, cache.head_dim)
         k = torch.empty(shape, dtype=dtype, device=cache.info.device)
-        v = torch.empty(shape, dtype=dtype, device=cache.info.device)
+        v = torch.empty_like(k)
     else:
         k, v = out
         if k.dim() != 3 or (n_tokens is not None and n_tokens != k.shape[0]):

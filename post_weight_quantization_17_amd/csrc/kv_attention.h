@@ -12,6 +12,7 @@ constexpr int ATT_WAVES = 4;
 constexpr int ATT_ROWS = 16;                     // query rows of a wave's MFMA
 constexpr int ATT_TILE = 32;                     // keys a wave takes at a time
 constexpr int ATT_MIN_CHUNK = 256;               // fewest keys of a workgroup when a row's keys are split
+constexpr int ATT_UNSPLIT = 512;                 // a table of at most so many keys is not split: a join costs 3 us
 constexpr int ATT_MAX_TARGET = 4 * 256;          // most workgroups that the keys are split for (Seq)
 constexpr int PROMPT_MAX_TARGET = 2 * 256;       // and in the prompts' kernel
 constexpr int64_t PROMPT_ROWS = 64;               // see cut_call
@@ -19,6 +20,23 @@ constexpr float ATT_W_TOP = 8.0f;                // log2 of the largest weight a
 constexpr float ATT_W_LIMIT = 32768.0f;          // a weight above this asks for the next one
 constexpr float ATT_LOWEST = -3.402823466e38f;   // M before the first key
 constexpr float LOG2E = 1.44269504088896340736f;
+
+// Division of 0 .. 2^31 - 1 by a number known on the host: with s = ceil(log2
+// d) and mul = floor(2^32 (2^s - d) / d) + 1, n / d = (n + floor(n mul / 2^32))
+// / 2^s rounded down.
+struct Divider {
+  uint32_t d, mul, shift;
+  static Divider by(uint32_t d) {
+    Divider r{d, 0, 0};
+    while ((uint64_t(1) << r.shift) < d) ++r.shift;
+    r.mul = uint32_t((((uint64_t(1) << r.shift) - d) << 32) / d) + 1;
+    return r;
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    const uint32_t t = uint32_t((uint64_t(uint32_t(n)) * mul) >> 32);
+    return int((t + uint32_t(n)) >> shift);
+  }
+};
 
 struct AttArgs {
   KvCache c;
@@ -33,7 +51,9 @@ struct AttArgs {
   float scale;  // of the scores, in log2 units
   int ratio;    // query heads that share a key-value head
   int q_dtype, out_dtype, q_vec, out_vec;
-  int block_rows;  // query rows of a row block
+  int block_shift; // log2 of a row block's query rows
+  Divider by_heads, by_ratio;  // kv_heads, ratio
+  int per_token;   // row blocks of one token, where each sequence has one
   int rows;     // most of them that a call has: those of a part
   int splits;   // 0: no row block's keys are split
   int units;    // of the launch
@@ -50,9 +70,9 @@ __device__ __forceinline__ void store_out(const AttArgs& a, int64_t at, float v)
     static_cast<float*>(a.out)[at] = v;
 }
 
-// The row blocks of a sequence with n new tokens.
-__host__ __device__ __forceinline__ int64_t row_blocks(int64_t n, int ratio, int rows) {
-  return (n * ratio + rows - 1) / rows;
+// The row blocks of 2^shift rows of a sequence with n new tokens.
+__host__ __device__ __forceinline__ int64_t row_blocks(int64_t n, int ratio, int shift) {
+  return (n * ratio + (int64_t(1) << shift) - 1) >> shift;
 }
 
 // A call's work is cut into units: one row block (of one key-value head) over
@@ -135,7 +155,7 @@ __device__ __forceinline__ Seq find_unit(const AttArgs& a, int at, int lane) {
     float work = 0.0f;
     for (int64_t b0 = 0; b0 < q.batch; b0 += 64) {
       const Span s = seq_span(q, b0 + lane);
-      work += float(row_blocks(s.n, a.ratio, a.block_rows)) * float(cached(s.len, cap));
+      work += float(row_blocks(s.n, a.ratio, a.block_shift)) * float(cached(s.len, cap));
     }
     work = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wave_prefix(work)), 63));
     constexpr uint32_t step = ATT_WAVES * ATT_TILE;
@@ -148,7 +168,7 @@ __device__ __forceinline__ Seq find_unit(const AttArgs& a, int at, int lane) {
     const Span s = seq_span(q, b0 + lane);
     const uint32_t keys = cached(s.len, cap);
     const int splits = a.splits && keys > r.chunk ? int((keys - 1) / r.chunk) + 1 : 1;
-    const int blocks = int(row_blocks(s.n, a.ratio, a.block_rows));
+    const int blocks = int(row_blocks(s.n, a.ratio, a.block_shift));
     // A sum past 2^24 is past the launch, whatever the arrays hold.
     const int64_t all = int64_t(blocks) * splits;
     const int units = int(all < (1 << 24) ? all : (1 << 24));
@@ -186,7 +206,7 @@ __device__ __forceinline__ uint32_t keys_seen(int64_t len, int n, int i, int64_t
   return uint32_t(end < 0 ? 0 : end > cap ? cap : end);
 }
 __device__ __forceinline__ int block_last_row(const AttArgs& a, int n, int rb) {
-  const int last = rb * a.block_rows + a.block_rows - 1, rows = n * a.ratio;
+  const int last = ((rb + 1) << a.block_shift) - 1, rows = n * a.ratio;
   return last < rows ? last : rows - 1;
 }
 

@@ -73,7 +73,7 @@ kv_attend(AttArgs a) {
   const KvCache& c = a.c;
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int g = lane / 16, n16 = lane % 16;
-  const int kv = int(blockIdx.x % unsigned(c.heads));
+  const int unit = a.by_heads(int(blockIdx.x)), kv = int(blockIdx.x) - unit * c.heads;
   // A tile's pages are the table entries of its two 16-key subtiles.
   struct Ids {
     int id[2];
@@ -83,8 +83,8 @@ kv_attend(AttArgs a) {
   const bool plain = !a.splits && !a.b.starts;  // one unit a row block, one token a sequence
   if (plain) {
     // The first tile's pages are known without the length: both loads at once.
-    const int at = int(blockIdx.x / unsigned(c.heads)), per = int(row_blocks(1, a.ratio, a.block_rows));
-    sq = Seq{at / per, at / per, 1, at % per, 0, 1, 0, 0, 0xFFFFFF80u};
+    const int b = a.per_token == 1 ? unit : unit / a.per_token;
+    sq = Seq{b, b, 1, unit - b * a.per_token, 0, 1, 0, 0, 0xFFFFFF80u};
     const int len_now = a.b.lens[sq.b];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -93,7 +93,7 @@ kv_attend(AttArgs a) {
     }
     sq.len = __builtin_amdgcn_readfirstlane(len_now);
   } else {
-    sq = find_unit<false>(a, int(blockIdx.x / unsigned(c.heads)), lane);
+    sq = find_unit<false>(a, unit, lane);
     if (sq.b < 0) return;  // whole workgroup; uniform
   }
 
@@ -101,7 +101,7 @@ kv_attend(AttArgs a) {
   const int64_t len = sq.len;
   const int last_row = block_last_row(a, sq.n, sq.rb);
   const int nrows = last_row - sq.rb * ATT_ROWS + 1;
-  const uint32_t kend = keys_seen(len, sq.n, last_row / a.ratio, cap);
+  const uint32_t kend = keys_seen(len, sq.n, a.by_ratio(last_row), cap);
   if (len > cap && threadIdx.x == 0) kv_flag(a.info);
   const uint32_t k0 = sq.split * sq.chunk;
   if (sq.split > 0 && k0 >= kend) return;
@@ -110,10 +110,10 @@ kv_attend(AttArgs a) {
   // This lane's query row, and the keys that every row of the block sees.
   const int row = sq.rb * ATT_ROWS + n16;
   const bool live = n16 < nrows;
-  const int i = live ? row / a.ratio : 0;
+  const int i = live ? a.by_ratio(row) : 0;
   const int hq = kv * a.ratio + (live ? row - i * a.ratio : 0);
   const uint32_t lim = live ? keys_seen(len, sq.n, i, cap) : 0;
-  const uint32_t all_see = keys_seen(len, sq.n, sq.rb * ATT_ROWS / a.ratio, cap);
+  const uint32_t all_see = keys_seen(len, sq.n, a.by_ratio(sq.rb * ATT_ROWS), cap);
   const int pos = int(len - sq.n + i);
   const float slope = a.slopes ? a.slopes[hq] * LOG2E : 0.0f;
 
@@ -405,8 +405,9 @@ kv_attend(AttArgs a) {
   }
   for (int r = wave; r < nrows; r += ATT_WAVES) {
     const int at = sq.rb * ATT_ROWS + r;
-    const int64_t t = sq.t0 + at / a.ratio;
-    const int h = kv * a.ratio + at % a.ratio;
+    const int tok = a.by_ratio(at);
+    const int64_t t = sq.t0 + tok;
+    const int h = kv * a.ratio + (at - tok * a.ratio);
     float top = lds_m[0][r];
     for (int w = 1; w < ATT_WAVES; ++w) top = fmaxf(top, lds_m[w][r]);
     float sum = 0.0f;
@@ -438,11 +439,11 @@ kv_join(AttArgs a, int rows) {
   __shared__ float tops[64], weights[64];
   const KvCache& c = a.c;
   const int lane = threadIdx.x % 64;
-  const int kv = int(blockIdx.x / unsigned(rows) % unsigned(c.heads));
-  const Seq sq = find_unit<true>(a, int(blockIdx.x / unsigned(rows) / unsigned(c.heads)), lane);
+  const int pair = int(blockIdx.x / unsigned(rows)), block = a.by_heads(pair), kv = pair - block * c.heads;
+  const Seq sq = find_unit<true>(a, block, lane);
   if (sq.b < 0) return;
   const int last_row = block_last_row(a, sq.n, sq.rb);
-  const uint32_t kend = keys_seen(sq.len, sq.n, last_row / a.ratio, a.b.max_pages << c.shift);
+  const uint32_t kend = keys_seen(sq.len, sq.n, a.by_ratio(last_row), a.b.max_pages << c.shift);
   if (kend <= sq.chunk) return;  // kv_attend wrote the rows
   const int active = int((kend - 1) / sq.chunk) + 1;
   if (sq.first + active > a.parts) return;  // only where starts are out of order
@@ -451,11 +452,11 @@ kv_join(AttArgs a, int rows) {
   const int per = quads <= 4 ? 4 : quads <= 8 ? 8 : quads <= 16 ? 16 : quads <= 32 ? 32 : 64;
   const int d4 = int(threadIdx.x) % per, residue = int(threadIdx.x) / per, residues = 64 * ATT_WAVES / per;
 
-  for (int r = int(blockIdx.x % unsigned(rows)); r <= last_row - sq.rb * a.block_rows; r += rows) {
+  for (int r = int(blockIdx.x) - pair * rows; r <= last_row - (sq.rb << a.block_shift); r += rows) {
     const int64_t pr = (int64_t(sq.first) * c.heads + kv) * a.rows + r;
-    const int row = sq.rb * a.block_rows + r;
-    const int64_t t = sq.t0 + row / a.ratio;
-    const int h = kv * a.ratio + row % a.ratio;
+    const int row = (sq.rb << a.block_shift) + r, tok = a.by_ratio(row);
+    const int64_t t = sq.t0 + tok;
+    const int h = kv * a.ratio + (row - tok * a.ratio);
     float4 o = {0.0f, 0.0f, 0.0f, 0.0f};
     float top = ATT_LOWEST, sum = 0.0f;
     const float4* src = reinterpret_cast<const float4*>(a.part_o) + pr * quads + (d4 < quads ? d4 : 0);
@@ -504,7 +505,7 @@ constexpr int64_t JOIN_GROUPS = 1024;  // workgroups of a join, or one a row blo
 // the types (workspace sizes are asked for without them).
 struct Cut {
   bool prompt;     // by the prompts' kernel
-  int block_rows;  // query rows of a row block
+  int block_shift; // log2 of a row block's query rows
   int rows;        // most of them in any
   int64_t blocks;  // at most this many row blocks (of each key-value head)
   int64_t chunks;  // at most this many chunks of any sequence's keys
@@ -515,10 +516,12 @@ Cut cut_call(const KvCache& c, const KvBatch& b, int ratio) {
   // The prompts' kernel converts the cache once for 8 waves of rows; it takes
   // the calls whose sequences have PROMPT_ROWS query rows in the mean.
   k.prompt = b.starts && b.n_tokens * ratio >= PROMPT_ROWS * b.batch;
-  k.block_rows = k.prompt ? PROMPT_BLOCK : ATT_ROWS;
-  k.rows = b.starts || ratio > k.block_rows ? k.block_rows : ratio;
-  k.blocks = b.starts ? row_blocks(b.n_tokens, ratio, k.block_rows) + b.batch : b.batch * row_blocks(1, ratio, k.block_rows);
-  k.chunks = ((b.max_pages << c.shift) + ATT_MIN_CHUNK - 1) / ATT_MIN_CHUNK;
+  k.block_shift = k.prompt ? 7 : 4;
+  static_assert(PROMPT_BLOCK == 1 << 7 && ATT_ROWS == 1 << 4, "rows of a row block");
+  k.rows = b.starts || ratio > 1 << k.block_shift ? 1 << k.block_shift : ratio;
+  k.blocks = b.starts ? row_blocks(b.n_tokens, ratio, k.block_shift) + b.batch : b.batch * row_blocks(1, ratio, k.block_shift);
+  const int64_t keys = b.max_pages << c.shift;
+  k.chunks = keys <= ATT_UNSPLIT ? 1 : (keys + ATT_MIN_CHUNK - 1) / ATT_MIN_CHUNK;
   const int64_t parts = 2 * (k.prompt ? PROMPT_MAX_TARGET : ATT_MAX_TARGET) / c.heads + 2;
   k.parts = k.chunks <= 1 ? 0 : parts / k.chunks < k.blocks ? parts : k.blocks * k.chunks;
   return k;
@@ -587,7 +590,10 @@ extern "C" int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch
   a.target = k.prompt ? prompt_target(dp, split) : 256 * att_waves_per_simd(cache->bits, dp, split);
   const int64_t units = call_units(k, a.c.heads, a.target);
   if (units * a.c.heads >= (int64_t(1) << 24)) return GPTQ_E_INVALID_ARG;
-  a.block_rows = k.block_rows;
+  a.block_shift = k.block_shift;
+  a.by_heads = Divider::by(uint32_t(a.c.heads));
+  a.by_ratio = Divider::by(uint32_t(a.ratio));
+  a.per_token = int(row_blocks(1, a.ratio, k.block_shift));
   a.rows = k.rows;
   a.splits = k.parts > 0;
   a.units = int(units);

@@ -45,15 +45,15 @@ kv_attend_rows(AttArgs a) {
   const KvCache& c = a.c;
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int g = lane / 16, n16 = lane % 16;
-  const int kv = int(blockIdx.x % unsigned(c.heads));
-  const Seq sq = find_unit<false>(a, int(blockIdx.x / unsigned(c.heads)), lane);
+  const int unit = a.by_heads(int(blockIdx.x)), kv = int(blockIdx.x) - unit * c.heads;
+  const Seq sq = find_unit<false>(a, unit, lane);
   if (sq.b < 0) return;  // whole workgroup; uniform
 
   const int64_t cap = a.b.max_pages << c.shift;
   const int64_t len = sq.len;
   const int last_row = block_last_row(a, sq.n, sq.rb);
-  const int nrows = last_row - sq.rb * a.block_rows + 1;
-  const uint32_t kend = keys_seen(len, sq.n, last_row / a.ratio, cap);
+  const int nrows = last_row - (sq.rb << a.block_shift) + 1;
+  const uint32_t kend = keys_seen(len, sq.n, a.by_ratio(last_row), cap);
   if (len > cap && threadIdx.x == 0) kv_flag(a.info);
   const uint32_t k0 = sq.split * sq.chunk;
   if (sq.split > 0 && k0 >= kend) return;
@@ -61,13 +61,13 @@ kv_attend_rows(AttArgs a) {
 
   // This lane's query row, and the keys that all and any of the wave's rows
   // see.
-  const int first = wave * 16, base_row = sq.rb * a.block_rows + first;
+  const int first = wave * 16, base_row = (sq.rb << a.block_shift) + first;
   const bool live = first + n16 < nrows;
-  const int at_row = live ? base_row + n16 : 0, i = at_row / a.ratio;
+  const int at_row = live ? base_row + n16 : 0, i = a.by_ratio(at_row);
   const int token = sq.t0 + i, head = kv * a.ratio + (at_row - i * a.ratio);
   const int pos = live ? int(len - sq.n + i) : -1;  // past no key where there is no row
-  const uint32_t all = first < nrows ? keys_seen(len, sq.n, base_row / a.ratio, cap) : 0;
-  const uint32_t any = first < nrows ? keys_seen(len, sq.n, (first + 15 < nrows ? base_row + 15 : last_row) / a.ratio, cap) : 0;
+  const uint32_t all = first < nrows ? keys_seen(len, sq.n, a.by_ratio(base_row), cap) : 0;
+  const uint32_t any = first < nrows ? keys_seen(len, sq.n, a.by_ratio(first + 15 < nrows ? base_row + 15 : last_row), cap) : 0;
   const float slope = a.slopes ? a.slopes[head] * LOG2E : 0.0f;
   Query<BITS, DP, FULL, SPLIT> q;
   q.load(a, live, token, head, g);
@@ -345,7 +345,7 @@ kv_attend_rows(AttArgs a) {
   // The row's place is worked out again rather than kept through the loop.
   uint32_t out_row = uint32_t(base_row + n16);
   KV_OPAQUE_V(out_row);
-  const int out_i = int(out_row) / a.ratio;
+  const int out_i = a.by_ratio(int(out_row));
   const int64_t out_at = int64_t(sq.t0 + out_i) * a.ldo + int64_t(kv * a.ratio + (int(out_row) - out_i * a.ratio)) * c.dim;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
