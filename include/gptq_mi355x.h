@@ -389,8 +389,8 @@ int gptq_dequant_matvec(const uint32_t* packed, const float* scales, const int32
  *            is, so that one word can collect over many calls. Nothing is
  *            read or written there.
  * Shared errors: NULL structs, buffers, table or lens; buffers not aligned;
- * page_size, head_dim or bits other than above; n_pages outside 1 .. 2^31 - 1,
- * kv_heads outside 1 .. 65535, batch or n_tokens outside 0 .. 2^25, max_pages
+ * page_size, head_dim or bits other than above; kv_heads outside 1 .. 65535,
+ * n_pages < 1 or n_pages * kv_heads > 2^31 - 1, batch or n_tokens outside 0 .. 2^25, max_pages
  * outside 1 .. 2^31 - 1, ld_table < max_pages; starts NULL and n_tokens !=
  * batch -> GPTQ_E_INVALID_ARG. n_tokens = 0 or batch = 0 does nothing.
  * ---------------------------------------------------------------------- */

@@ -306,6 +306,28 @@ __device__ __forceinline__ void load_words(const char* p, uint32_t* w) {
   }
 }
 
+// Where 16 keys of a head lie, as byte offsets into the codes and the grids
+// (the same for k and v). The host has checked that pages times heads fit 31
+// bits, so one 32-bit product and one widening product each suffice. Keys
+// outside the cache's pages (flagged where they count, p < k1) get the first
+// page's: those are there to be read, and are masked.
+struct Place16 {
+  uint64_t codes, grid;
+  uint32_t ok;
+  __device__ __forceinline__ Place16 next(int words) const { return Place16{codes + 64u * uint32_t(words), grid + 64u, ok}; }
+};
+__device__ __forceinline__ Place16 place16(const KvCache& c, int32_t* info, int kv, int page, uint32_t p, uint32_t k1) {
+  uint32_t id = uint32_t(__builtin_amdgcn_readfirstlane(page));
+  const uint32_t ok = id < uint32_t(c.n_pages);
+  if (!ok) {
+    if (p < k1) kv_flag(info);
+    id = 0;
+  }
+  const uint32_t head = id * uint32_t(c.heads) + uint32_t(kv), in = p & ((1u << c.shift) - 1);
+  const uint32_t row = 4u * uint32_t(c.words);
+  return Place16{uint64_t(head) * (row << c.shift) + in * row, uint64_t(head) * (4u << c.shift) + 4u * in, ok};
+}
+
 // A lane's part of a query row as the B operand of the first product: its
 // blocks of 8 elements, in the order of the codes, scaled to a largest element
 // of 2^13 to 2^14 and split in two parts where SPLIT; their sum, for the

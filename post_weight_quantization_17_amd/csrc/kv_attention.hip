@@ -124,34 +124,20 @@ kv_attend(AttArgs a) {
   constexpr uint32_t step = ATT_WAVES * ATT_TILE;
   const int words = FULL ? DP * BITS / 32 : c.words;
   const int32_t* const pages = a.b.table + sq.b * a.b.ld;
+  const bool one_page = c.shift >= 5;  // a tile's keys lie on one page
   const auto look_up = [&](uint32_t p0) {
     Ids r{{-1, -1}};
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-      if (p0 + 16 * u < k1) r.id[u] = pages[(p0 + 16 * u) >> c.shift];
+    if (p0 < k1) r.id[0] = pages[p0 >> c.shift];
+    if (!one_page && p0 + 16 < k1) r.id[1] = pages[(p0 + 16) >> c.shift];
     return r;
   };
-  // Cache row of each 16-key subtile's first key, and which subtiles (bit u)
-  // lie on a page. The others read the first page's rows and are masked.
   struct Rows {
-    int64_t at[2];
-    uint32_t ok;
+    Place16 u[2];
   };
   const auto locate = [&](uint32_t p0, const Ids& ids) {
     Rows r;
-    r.ok = 0;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint32_t p = p0 + 16 * u;
-      int64_t id = __builtin_amdgcn_readfirstlane(ids.id[u]);
-      if (id >= 0 && id < c.n_pages) {
-        r.ok |= 1u << u;
-      } else {
-        if (p < k1) kv_flag(a.info);
-        id = 0;
-      }
-      r.at[u] = ((id * c.heads + kv) << c.shift) + (p & ((1u << c.shift) - 1));
-    }
+    r.u[0] = place16(c, a.info, kv, ids.id[0], p0, k1);
+    r.u[1] = one_page ? r.u[0].next(words) : place16(c, a.info, kv, ids.id[1], p0 + 16, k1);
     return r;
   };
   const int vc = n16 * DPL < c.dim ? n16 : 0;  // lanes past the head's end repeat the first one's codes
@@ -168,8 +154,8 @@ kv_attend(AttArgs a) {
     KV_FRESH_V(quad_off);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const char* kr = reinterpret_cast<const char*>(c.k_codes + at.at[u] * words);
-      const char* gr = reinterpret_cast<const char*>(c.k_grid + at.at[u]);
+      const char* kr = reinterpret_cast<const char*>(c.k_codes) + at.u[u].codes;
+      const char* gr = reinterpret_cast<const char*>(c.k_grid) + at.u[u].grid;
       if constexpr (FULL) {
         load_words<KW>(kr + k_off, t.k[u]);
       } else {
@@ -187,8 +173,8 @@ kv_attend(AttArgs a) {
     KV_FRESH_V(quad_off);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      t.vg[u] = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(c.v_grid + at.at[u]) + quad_off);
-      const char* vr = reinterpret_cast<const char*>(c.v_codes + at.at[u] * words);
+      t.vg[u] = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(c.v_grid) + at.u[u].grid + quad_off);
+      const char* vr = reinterpret_cast<const char*>(c.v_codes) + at.u[u].codes;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const char* vp = vr + 4 * r * words + v_off;
@@ -220,7 +206,7 @@ kv_attend(AttArgs a) {
   const Consts kc = conversion_consts<BITS>();
 
   while (p0 < k1) {
-    const uint32_t ok = at.ok;
+    const uint32_t ok = at.u[0].ok | at.u[1].ok << 1;
     const bool more = p0 + step < k1;
     float x[8], sv[8];
 #pragma unroll

@@ -170,7 +170,7 @@ inline int kv_views(const gptq_kv_cache* c, const gptq_kv_batch* b, KvCache* cv,
   if (c->head_dim < 16 || c->head_dim > 256 || c->head_dim % 16 != 0) return GPTQ_E_INVALID_ARG;
   if (c->kv_heads < 1 || c->kv_heads > 65535) return GPTQ_E_INVALID_ARG;
   if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) != 0) return GPTQ_E_INVALID_ARG;
-  if (c->n_pages < 1 || c->n_pages > INT32_MAX) return GPTQ_E_INVALID_ARG;
+  if (c->n_pages < 1 || c->n_pages > INT32_MAX / c->kv_heads) return GPTQ_E_INVALID_ARG;
   if (b->batch < 0 || b->n_tokens < 0 || b->max_pages < 1 || b->ld_table < b->max_pages) return GPTQ_E_INVALID_ARG;
   if (b->batch > KV_MAX_TOKENS || b->n_tokens > KV_MAX_TOKENS || b->max_pages > INT32_MAX) return GPTQ_E_INVALID_ARG;
   if (b->batch > 0 && (!b->table || !b->lens)) return GPTQ_E_INVALID_ARG;

@@ -20,7 +20,7 @@ constexpr int ROWS_WAVES = 8;
 static_assert(PROMPT_BLOCK == 16 * ROWS_WAVES, "a block's rows are its waves' tiles");
 // A workgroup has two waves on each SIMD; two workgroups share a CU where 128
 // registers suffice.
-constexpr int prompt_waves_per_simd(int dp, bool split) { return dp <= 128 && !split ? 4 : 2; }
+constexpr int prompt_waves_per_simd(int dp, bool split) { return dp == 64 || (dp == 128 && !split) ? 4 : 2; }
 
 constexpr int ROWS_TILE = 64;  // keys at a time
 
@@ -29,6 +29,7 @@ struct Stage {
   half8 k[4][DP / 32][64];  // [16 keys][32 d][lane]
   half8 v[2][DP / 16][64];  // [32 keys][d within a lane's share][lane]
   float sk[64], sv[64];     // scales of the keys
+  uint32_t ok[4];           // whether 16 keys lie on a page
 };
 
 template <int BITS, int DP, bool FULL, bool SPLIT>
@@ -79,17 +80,21 @@ kv_attend_rows(AttArgs a) {
   const int part = wave & 1, span = wave >> 1 & 1;
   struct Raw {
     uint32_t w[KW > 8 * VW ? KW : 8 * VW];
-    uint4 zg[2];      // values: grids of this lane's 8 keys; keys: of key n16, of k and v
-    uint32_t ok;      // bit u: the 16 keys u lie on a page
+    uint4 zg[2];  // values: grids of this lane's 8 keys; keys: of key n16, of k and v
+    uint32_t ok;  // keys: they lie on a page
   };
+  // The pages of the keys that this wave converts: of its 16, or of the two
+  // 16s of its 32 (one page if that holds them).
+  const int ahead = wave < 4 ? 16 * wave : 32 * span;
+  const bool one_page = wave < 4 || c.shift >= 5;
   struct Ids {
-    int id[4];
+    int id[2];
   };
   const auto look_up = [&](uint32_t p0) {
-    Ids r{{-1, -1, -1, -1}};
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (p0 + 16 * u < k1) r.id[u] = pages[(p0 + 16 * u) >> c.shift];
+    Ids r{{-1, -1}};
+    const uint32_t p = p0 + ahead;
+    if (p < k1) r.id[0] = pages[p >> c.shift];
+    if (!one_page && p + 16 < k1) r.id[1] = pages[(p + 16) >> c.shift];
     return r;
   };
   const int vc = n16 * DPL < c.dim ? n16 : 0;  // lanes past the head's end repeat the first one's codes
@@ -97,20 +102,9 @@ kv_attend_rows(AttArgs a) {
   uint32_t k_off = FULL ? 4u * (n16 * words + g * KW) : 4u * n16 * words;
   uint32_t key_off = 4u * n16, quad_off = 16u * g;  // of grid words
   const auto fetch = [&](uint32_t p0, const Ids& ids, Raw& raw) {
-    int64_t at[4];
-    raw.ok = 0;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t p = p0 + 16 * u;
-      int64_t id = __builtin_amdgcn_readfirstlane(ids.id[u]);
-      if (id >= 0 && id < c.n_pages) {
-        raw.ok |= 1u << u;
-      } else {
-        if (p < k1) kv_flag(a.info);
-        id = 0;  // masked; the first page's rows are there to be read
-      }
-      at[u] = ((id * c.heads + kv) << c.shift) + (p & ((1u << c.shift) - 1));
-    }
+    const uint32_t p = p0 + ahead;
+    const Place16 first = place16(c, a.info, kv, ids.id[0], p, k1);
+    raw.ok = first.ok;
     // Base pointers are uniform, offsets 32 bits a lane; their sums are formed
     // by the loads.
     KV_FRESH_V(v_off);
@@ -118,26 +112,28 @@ kv_attend_rows(AttArgs a) {
     KV_FRESH_V(key_off);
     KV_FRESH_V(quad_off);
     if (wave < 4) {
-      const int64_t mine = wave == 0 ? at[0] : wave == 1 ? at[1] : wave == 2 ? at[2] : at[3];
-      const char* kr = reinterpret_cast<const char*>(c.k_codes + mine * words);
-      raw.zg[0].x = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const char*>(c.k_grid + mine) + key_off);
-      raw.zg[0].y = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const char*>(c.v_grid + mine) + key_off);
+      const char* kr = reinterpret_cast<const char*>(c.k_codes) + first.codes;
+      raw.zg[0].x = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const char*>(c.k_grid) + first.grid + key_off);
+      raw.zg[0].y = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const char*>(c.v_grid) + first.grid + key_off);
       if constexpr (FULL) {
         load_words<KW>(kr + k_off, raw.w);
       } else {
         constexpr int W = BITS / 4;  // words of a block of 8 d
+        uint32_t fresh_g = g;        // the blocks' offsets are formed here, not kept
+        KV_FRESH_V(fresh_g);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-          const int b = lane_block<DP, FULL>(g, j);
+          const int b = lane_block<DP, FULL>(int(fresh_g), j);
           load_words<W>(kr + (k_off + 4u * W * (8 * b < c.dim ? b : 0)), &raw.w[W * j]);
         }
       }
     } else {
+      const Place16 second = one_page ? first.next(words) : place16(c, a.info, kv, ids.id[1], p + 16, k1);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int64_t base = span ? at[2 + u] : at[u];
-        raw.zg[u] = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(c.v_grid + base) + quad_off);
-        const char* vr = reinterpret_cast<const char*>(c.v_codes + base * words);
+        const Place16& at = u ? second : first;
+        raw.zg[u] = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(c.v_grid) + at.grid + quad_off);
+        const char* vr = reinterpret_cast<const char*>(c.v_codes) + at.codes;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const char* vp = vr + 4 * r * words + v_off;
@@ -173,6 +169,7 @@ kv_attend_rows(AttArgs a) {
       if (g == 0) {
         st.sk[16 * wave + n16] = kv_scale(raw.zg[0].x);
         st.sv[16 * wave + n16] = kv_scale(raw.zg[0].y);
+        st.ok[wave] = raw.ok;
       }
       return;
     }
@@ -214,8 +211,9 @@ kv_attend_rows(AttArgs a) {
 #pragma unroll
   for (int m = 0; m < DPL; ++m) o[m] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // 32 of the tile's keys (half h) from p0 on; ok: bit u for its 16 keys u.
-  const auto compute = [&](uint32_t p0, uint32_t ok, const Stage<DP>& st, int half) {
+  // 32 of the tile's keys (half h) from p0 on.
+  const auto compute = [&](uint32_t p0, const Stage<DP>& st, int half) {
+    const uint32_t ok = __builtin_amdgcn_readfirstlane(st.ok[2 * half] | st.ok[2 * half + 1] << 1);
     float x[8], s[8];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -297,7 +295,6 @@ kv_attend_rows(AttArgs a) {
     Ids ids = look_up(k0);
     fetch(k0, ids, raw);
     ids = look_up(k0 + ROWS_TILE);
-    uint32_t ok = raw.ok;
     convert(raw, stage[0]);
     if (k0 + ROWS_TILE < k1) {
       fetch(k0 + ROWS_TILE, ids, raw);
@@ -306,9 +303,7 @@ kv_attend_rows(AttArgs a) {
     __syncthreads();
     int b = 0;
     for (uint32_t p0 = k0; p0 < k1; p0 += ROWS_TILE, b ^= 1) {
-      uint32_t next_ok = 0;
       if (p0 + ROWS_TILE < k1) {
-        next_ok = raw.ok;
         convert(raw, stage[b ^ 1]);
         if (p0 + 2 * ROWS_TILE < k1) {
           fetch(p0 + 2 * ROWS_TILE, ids, raw);
@@ -317,8 +312,7 @@ kv_attend_rows(AttArgs a) {
       }
 #pragma unroll 1
       for (int h = 0; h < 2; ++h)
-        if (p0 + 32 * h < any) compute(p0 + 32 * h, ok >> (2 * h) & 3u, stage[b], h);
-      ok = next_ok;
+        if (p0 + 32 * h < any) compute(p0 + 32 * h, stage[b], h);
       __syncthreads();
     }
   }
