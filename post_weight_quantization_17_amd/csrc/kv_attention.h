@@ -14,8 +14,7 @@ constexpr int ATT_TILE = 32;                     // keys a wave takes at a time
 constexpr int ATT_MIN_CHUNK = 256;               // fewest keys of a workgroup when a row's keys are split
 constexpr int ATT_UNSPLIT = 512;                 // a table of at most so many keys is not split: a join costs 3 us
 constexpr int ATT_MAX_TARGET = 4 * 256;          // most workgroups that the keys are split for (Seq)
-constexpr int PROMPT_MAX_TARGET = 2 * 256;       // and in the prompts' kernel
-constexpr int64_t PROMPT_ROWS = 64;               // see cut_call
+constexpr int PROMPT_TARGET = 256;               // and in the prompts' kernel
 constexpr float ATT_W_TOP = 8.0f;                // log2 of the largest weight after a rescaling
 constexpr float ATT_W_LIMIT = 32768.0f;          // a weight above this asks for the next one
 constexpr float ATT_LOWEST = -3.402823466e38f;   // M before the first key
@@ -384,7 +383,6 @@ struct Query {
 
 // The prompts' kernel (kv_prompt.hip).
 constexpr int PROMPT_BLOCK = 128;  // query rows of its row blocks
-int prompt_target(int dp, bool split);
 int launch_prompt(const AttArgs& a, int bits, bool split, hipStream_t s);
 
 }  // namespace gptq

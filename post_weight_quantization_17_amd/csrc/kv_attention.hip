@@ -487,6 +487,16 @@ kv_join(AttArgs a, int rows) {
 
 constexpr int64_t JOIN_GROUPS = 1024;  // workgroups of a join, or one a row block if those are more
 
+// Least query rows (over all heads) of a call for the prompts' kernel, which
+// also asks for a whole row block a sequence in the mean. It converts the cache
+// once for 128 rows, but needs many row blocks to fill the GPU and to balance
+// the causal mask. Measured (us, prompts' kernel and the other; 2000 cached
+// tokens; rows are tokens times query heads):
+//   8 sequences, 32 heads over 8, 4 bits:  32768 rows  98 / 104, 65536 rows 114 / 196
+//   8 sequences, 32 heads, 8 bits:         32768 rows 142 / 129, 49152 rows 138 / 183
+//   1 sequence, 32 heads over 8, 4 bits:    8192 rows  52 /  58,  4096 rows  39 /  34
+constexpr int64_t PROMPT_MIN_ROWS = 384 * PROMPT_BLOCK;
+
 // How a call is cut: everything that does not depend on device data, nor on
 // the types (workspace sizes are asked for without them).
 struct Cut {
@@ -497,18 +507,18 @@ struct Cut {
   int64_t chunks;  // at most this many chunks of any sequence's keys
   int64_t parts;   // at most this many partial results
 };
-Cut cut_call(const KvCache& c, const KvBatch& b, int ratio) {
+Cut cut_call(const KvCache& c, const KvBatch& b, int ratio, int64_t prompt_min_rows) {
   Cut k;
-  // The prompts' kernel converts the cache once for 8 waves of rows; it takes
-  // the calls whose sequences have PROMPT_ROWS query rows in the mean.
-  k.prompt = b.starts && b.n_tokens * ratio >= PROMPT_ROWS * b.batch;
+  const int64_t rows = b.n_tokens * ratio;
+  const int64_t each = prompt_min_rows < PROMPT_BLOCK ? prompt_min_rows : PROMPT_BLOCK;
+  k.prompt = b.starts && rows * c.heads >= prompt_min_rows && rows >= each * b.batch;
   k.block_shift = k.prompt ? 7 : 4;
   static_assert(PROMPT_BLOCK == 1 << 7 && ATT_ROWS == 1 << 4, "rows of a row block");
   k.rows = b.starts || ratio > 1 << k.block_shift ? 1 << k.block_shift : ratio;
   k.blocks = b.starts ? row_blocks(b.n_tokens, ratio, k.block_shift) + b.batch : b.batch * row_blocks(1, ratio, k.block_shift);
   const int64_t keys = b.max_pages << c.shift;
   k.chunks = keys <= ATT_UNSPLIT ? 1 : (keys + ATT_MIN_CHUNK - 1) / ATT_MIN_CHUNK;
-  const int64_t parts = 2 * (k.prompt ? PROMPT_MAX_TARGET : ATT_MAX_TARGET) / c.heads + 2;
+  const int64_t parts = 2 * (k.prompt ? PROMPT_TARGET : ATT_MAX_TARGET) / c.heads + 2;
   k.parts = k.chunks <= 1 ? 0 : parts / k.chunks < k.blocks ? parts : k.blocks * k.chunks;
   return k;
 }
@@ -537,24 +547,20 @@ int launch_attend(const AttArgs& a, bool split, hipStream_t s) {
   return launch_attend<BITS, 256>(a, split, s);
 }
 
-}  // namespace
-}  // namespace gptq
-
-using namespace gptq;
-
-extern "C" size_t gptq_kv_attention_workspace_size(const gptq_kv_cache* cache, const gptq_kv_batch* batch,
-                                                   int64_t q_heads) {
+size_t attention_workspace(const gptq_kv_cache* cache, const gptq_kv_batch* batch, int64_t q_heads,
+                           int64_t prompt_min_rows) {
   KvCache c;
   KvBatch b;
   if (kv_views(cache, batch, &c, &b) != GPTQ_OK || q_heads < 1 || q_heads % c.heads != 0) return 0;
   if (b.batch == 0 || b.n_tokens == 0) return 0;
-  const Cut k = cut_call(c, b, int(q_heads / c.heads));
+  const Cut k = cut_call(c, b, int(q_heads / c.heads), prompt_min_rows);
   return size_t(k.parts) * size_t(c.heads) * size_t(k.rows) * (size_t(c.dim) * sizeof(float) + sizeof(float2));
 }
 
-extern "C" int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const void* q, int q_dtype,
-                                 int64_t q_heads, int64_t ldq, double scale, const float* slopes, void* out,
-                                 int out_dtype, int64_t ldo, void* ws, size_t ws_bytes, int32_t* info, void* stream) {
+// gptq_kv_attention with the rows from which on the prompts' kernel runs.
+int attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const void* q, int q_dtype, int64_t q_heads,
+              int64_t ldq, double scale, const float* slopes, void* out, int out_dtype, int64_t ldo, void* ws,
+              size_t ws_bytes, int32_t* info, void* stream, int64_t prompt_min_rows) {
   AttArgs a{};
   int st = kv_views(cache, batch, &a.c, &a.b);
   if (st != GPTQ_OK) return st;
@@ -569,11 +575,13 @@ extern "C" int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch
     return GPTQ_E_INVALID_ARG;
   if (a.b.n_tokens == 0 || a.b.batch == 0) return GPTQ_OK;
   a.ratio = int(q_heads / a.c.heads);
-  const Cut k = cut_call(a.c, a.b, a.ratio);
+  const Cut k = cut_call(a.c, a.b, a.ratio, prompt_min_rows);
   const bool split = q_dtype == GPTQ_F32 || out_dtype == GPTQ_F32;
-  // One round of resident workgroups is what the keys are split for.
+  // One round of resident workgroups is what the keys are split for; prompts
+  // have that many row blocks, and split only where a sequence is far longer
+  // than the others.
   const int dp = a.c.dim <= 64 ? 64 : a.c.dim <= 128 ? 128 : 256;
-  a.target = k.prompt ? prompt_target(dp, split) : 256 * att_waves_per_simd(cache->bits, dp, split);
+  a.target = k.prompt ? PROMPT_TARGET : 256 * att_waves_per_simd(cache->bits, dp, split);
   const int64_t units = call_units(k, a.c.heads, a.target);
   if (units * a.c.heads >= (int64_t(1) << 24)) return GPTQ_E_INVALID_ARG;
   a.block_shift = k.block_shift;
@@ -596,7 +604,7 @@ extern "C" int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch
   a.q_vec = kv_vec16(q, ldq, q_dtype);
   a.out_vec = kv_vec16(out, ldo, out_dtype);
   if (a.splits) {
-    if (ws_bytes < gptq_kv_attention_workspace_size(cache, batch, q_heads)) return GPTQ_E_WORKSPACE;
+    if (ws_bytes < attention_workspace(cache, batch, q_heads, prompt_min_rows)) return GPTQ_E_WORKSPACE;
     if (!ws || reinterpret_cast<uintptr_t>(ws) % 16 != 0) return GPTQ_E_INVALID_ARG;
     a.part_o = static_cast<float*>(ws);  // its rows stay 16-byte aligned: head_dim is a multiple of 16
     a.part_ml = reinterpret_cast<float2*>(a.part_o + k.parts * a.c.heads * a.rows * a.c.dim);
@@ -613,4 +621,21 @@ extern "C" int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch
   const int rows = most * a.rows <= JOIN_GROUPS ? a.rows : int((JOIN_GROUPS + most - 1) / most);
   hipLaunchKernelGGL(kv_join, dim3(unsigned(most * rows)), dim3(64 * ATT_WAVES), 0, s, a, rows);
   return launch_status();
+}
+
+}  // namespace
+}  // namespace gptq
+
+using namespace gptq;
+
+extern "C" size_t gptq_kv_attention_workspace_size(const gptq_kv_cache* cache, const gptq_kv_batch* batch,
+                                                   int64_t q_heads) {
+  return attention_workspace(cache, batch, q_heads, PROMPT_MIN_ROWS);
+}
+
+extern "C" int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const void* q, int q_dtype,
+                                 int64_t q_heads, int64_t ldq, double scale, const float* slopes, void* out,
+                                 int out_dtype, int64_t ldo, void* ws, size_t ws_bytes, int32_t* info, void* stream) {
+  return attention(cache, batch, q, q_dtype, q_heads, ldq, scale, slopes, out, out_dtype, ldo, ws, ws_bytes, info, stream,
+                   PROMPT_MIN_ROWS);
 }

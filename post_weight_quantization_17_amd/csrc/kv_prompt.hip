@@ -386,8 +386,6 @@ int launch_rows(const AttArgs& a, bool split, hipStream_t s) {
 
 }  // namespace
 
-int prompt_target(int dp, bool split) { return 128 * prompt_waves_per_simd(dp, split); }
-
 int launch_prompt(const AttArgs& a, int bits, bool split, hipStream_t s) {
   return bits == 4 ? launch_rows<4>(a, split, s) : launch_rows<8>(a, split, s);
 }

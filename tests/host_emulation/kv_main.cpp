@@ -7,10 +7,12 @@
 //   kv_host <dir>
 //
 // <dir>/args.txt: op n_pages page_size kv_heads head_dim bits max_pages ld_table
-//   batch n_tokens starts q_heads dtype out_dtype ld ld_out offset scale slopes
+//   batch n_tokens starts q_heads dtype out_dtype ld ld_out offset scale slopes prompt_min_rows
 //   op: write, read or attend; starts, slopes: 0 or 1; ld, ld_out: token
 //   strides of the dense inputs and outputs; offset: elements by which the
-//   dense buffers are shifted inside their allocations.
+//   dense buffers are shifted inside their allocations; prompt_min_rows: query
+//   rows from which on attend runs the prompts' kernel, -1: the entry point's
+//   own rule (which asks for more than a CPU run can hold).
 // Inputs (.bin): k_codes v_codes k_grid v_grid table lens [starts], and k v or
 // q [slopes]; outputs: the cache's buffers after a write, k_out v_out or out
 // (filled with 0xA5 bytes beforehand), info. Every buffer is its own
@@ -64,12 +66,13 @@ int main(int argc, char** argv) {
   char op[16];
   long long n_pages, page_size, kv_heads, head_dim, max_pages, ld_table, batch, n_tokens, q_heads, ld, ld_out;
   int bits, starts, dtype, out_dtype, offset, slopes;
+  long long min_rows;
   double scale;
   {
     FILE* f = std::fopen((dir + "/args.txt").c_str(), "r");
-    if (!f || std::fscanf(f, "%15s %lld %lld %lld %lld %d %lld %lld %lld %lld %d %lld %d %d %lld %lld %d %lf %d", op,
+    if (!f || std::fscanf(f, "%15s %lld %lld %lld %lld %d %lld %lld %lld %lld %d %lld %d %d %lld %lld %d %lf %d %lld", op,
                           &n_pages, &page_size, &kv_heads, &head_dim, &bits, &max_pages, &ld_table, &batch, &n_tokens,
-                          &starts, &q_heads, &dtype, &out_dtype, &ld, &ld_out, &offset, &scale, &slopes) != 19)
+                          &starts, &q_heads, &dtype, &out_dtype, &ld, &ld_out, &offset, &scale, &slopes, &min_rows) != 20)
       return 2;
     std::fclose(f);
   }
@@ -104,11 +107,17 @@ int main(int argc, char** argv) {
     Buf sl{};
     if (slopes) sl = slurp("slopes");
     const Buf out = make(n_tokens ? size_t((n_tokens - 1) * ld_out + q_heads * head_dim) * eo : 0, offset * eo);
-    const size_t wsb = gptq_kv_attention_workspace_size(&cache, &b, q_heads);
+    const int64_t from = min_rows < 0 ? gptq::PROMPT_MIN_ROWS : min_rows;
+    const size_t wsb = min_rows < 0 ? gptq_kv_attention_workspace_size(&cache, &b, q_heads)
+                                    : gptq::attention_workspace(&cache, &b, q_heads, from);
     const Buf ws = make(wsb);
     std::memset(ws.at(), 0xFF, wsb);  // NaN: a partial sum that was not written shows
-    rc = gptq_kv_attention(&cache, &b, q.at(), dtype, q_heads, ld, scale, slopes ? sl.as<float>() : nullptr, out.at(),
-                           out_dtype, ld_out, wsb ? ws.at() : nullptr, wsb, info.as<int32_t>(), nullptr);
+    const float* sp = slopes ? sl.as<float>() : nullptr;
+    void* wp = wsb ? ws.at() : nullptr;
+    rc = min_rows < 0 ? gptq_kv_attention(&cache, &b, q.at(), dtype, q_heads, ld, scale, sp, out.at(), out_dtype, ld_out, wp,
+                                          wsb, info.as<int32_t>(), nullptr)
+                      : gptq::attention(&cache, &b, q.at(), dtype, q_heads, ld, scale, sp, out.at(), out_dtype, ld_out, wp,
+                                        wsb, info.as<int32_t>(), nullptr, from);
     spill("out", out);
   }
   spill("info", info);

@@ -124,7 +124,7 @@ ATTEND = [
     (80, 4, 32, 2, 2, [61], [61], "f32", "f32", False, None),
     (256, 8, 32, 1, 2, [70], [17], "f16", "f16", False, None),
     (128, 8, 16, 1, 1, [40 + i for i in range(70)], [1 + i % 2 for i in range(70)], "f16", "f16", False, None),
-    # 64 query rows a sequence or more in the mean: the prompts' kernel
+    # more rows
     (128, 8, 16, 2, 2, [333], [333], "bf16", "bf16", False, None),
     (64, 4, 64, 1, 4, [500, 0, 20], [133, 0, 20], "f16", "f16", True, None),
     (64, 8, 16, 3, 3, [130], [129], "f32", "f32", False, None),
@@ -136,6 +136,16 @@ ATTEND = [
     (16, 4, 16, 2, 64, [9], [2], "f16", "f32", False, None),
     (48, 8, 64, 1, 5, [1500], [21], "bf16", "bf16", False, None),
     (128, 4, 64, 1, 4, [3000, 100], [40, 5], "f16", "f16", False, None),
+    # 49152 query rows over all heads or more: the prompts' kernel
+    (128, 4, 64, 8, 64, [300, 130, 0, 77, 140, 64, 130], [250, 130, 0, 77, 140, 64, 120], "f16", "f16", False, None),
+    (64, 8, 16, 4, 64, [400, 390, 30], [390, 380, 30], "bf16", "bf16", True, None),
+    (256, 4, 32, 8, 64, [420, 390], [400, 380], "f16", "bf16", False, None),
+    (80, 8, 128, 32, 64, [450, 361, 3], [430, 361, 5], "bf16", "f16", True, None),
+    (128, 8, 16, 3, 48, [600, 500], [550, 500], "f32", "f32", False, None),
+    (112, 4, 16, 96, 96, [530, 17], [520, 10], "f16", "f16", False, None),
+    (16, 4, 16, 2, 256, [150, 60], [140, 60], "f32", "f16", False, None),
+    # a sequence far longer than the others: its row blocks' keys are split
+    (128, 4, 64, 8, 64, [2600, 300, 300, 300], [40, 250, 250, 250], "f16", "f16", True, None),
 ]
 
 
@@ -205,7 +215,7 @@ def test_vectors_that_are_not_finite(gpu):
     assert not np.isfinite(out[1, 0]).any()
 
 
-@pytest.mark.parametrize("ratio", [2, 40])  # 40: the prompts' kernel
+@pytest.mark.parametrize("ratio", [2, 40])
 def test_bad_pages_and_lengths_set_info(gpu, ratio):
     """(tests/test_kv_cache_host.py runs these and worse under a sanitizer.)"""
     rng = np.random.default_rng(7)

@@ -56,7 +56,7 @@ def kv_host(tmp_path_factory):
 
 
 def run(kv_host, name, op, cache, table, lens, starts, n_tokens, dtype="f16", out_dtype="f16", ld=0, ld_out=0, offset=0,
-        q_heads=1, scale=1.0, slopes=None, **arrays):
+        q_heads=1, scale=1.0, slopes=None, min_rows=-1, **arrays):
     exe, work = kv_host
     d = os.path.join(str(work), name)
     os.makedirs(d)
@@ -71,7 +71,7 @@ def run(kv_host, name, op, cache, table, lens, starts, n_tokens, dtype="f16", ou
     with open(os.path.join(d, "args.txt"), "w") as f:
         print(op, pages, page, heads, cache["head_dim"], cache["bits"], table.shape[1], table.shape[1], len(lens), n_tokens,
               int(starts is not None), q_heads, C.CODE[dtype], C.CODE[out_dtype], ld, ld_out, offset, repr(float(scale)),
-              int(slopes is not None), file=f)
+              int(slopes is not None), min_rows, file=f)
     env = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:halt_on_error=1", UBSAN_OPTIONS="print_stacktrace=1")
     p = subprocess.run([exe, d], capture_output=True, text=True, env=env, timeout=600)
     assert p.returncode == 0, f"{name}: exit {p.returncode}\n{p.stderr[-6000:]}"
@@ -185,7 +185,7 @@ ATTEND = [
     (192, 4, 16, 1, 2, [30, 4], [3, 6], "bf16", "bf16", False, None),  # rows before the sequence's start
     (48, 8, 16, 1, 1, [600], [1], "f16", "f16", False, None),  # split over workgroups
     (128, 4, 128, 1, 4, [700, 290], [2, 1], "bf16", "f16", True, True),  # split, ragged
-    # the prompts' kernel: 64 query rows a sequence or more in the mean
+    # the prompts' kernel (from PROMPTS on)
     (128, 4, 16, 1, 2, [75], [40], "f16", "f16", False, None),
     (64, 8, 32, 1, 4, [50, 20], [33, 20], "bf16", "bf16", False, None),
     (256, 4, 16, 1, 1, [70], [66], "f16", "f16", False, None),
@@ -194,6 +194,9 @@ ATTEND = [
     (48, 8, 64, 1, 1, [600], [70], "bf16", "f16", False, None),  # split over workgroups
     (192, 8, 16, 1, 1, [66, 3], [66, 65], "f16", "bf16", False, None),  # rows before the sequence's start
 ]
+
+
+PROMPTS = 9
 
 
 @pytest.mark.parametrize("case", range(len(ATTEND)))
@@ -207,7 +210,7 @@ def test_attention_runs_in_bounds_and_matches_the_oracle(kv_host, case):
     qf, qs = C.cast(1.5 * rng.standard_normal((n, hq, dim)), qdt)
     slopes = (2.0 ** -rng.uniform(1, 8, hq)).astype(np.float32) if use_slopes else None
     rd = run(kv_host, f"a{case}", "attend", cache, table, lens, starts, n, dtype=qdt, out_dtype=odt, ld=hq * dim,
-             ld_out=hq * dim + 3, q_heads=hq, scale=dim**-0.5, slopes=slopes, q=qs)
+             ld_out=hq * dim + 3, q_heads=hq, scale=dim**-0.5, slopes=slopes, q=qs, min_rows=1 if case >= PROMPTS else -1)
     ref, mag, written, bad = K.attention(qf, cache, table, lens, starts, dim**-0.5, slopes)
     got, _ = rows(rd("out", STORAGE[odt]), n, hq * dim + 3, hq * dim, odt)
     assert int(rd("info", np.int32)[0]) == int(bad) == 0
@@ -255,10 +258,10 @@ def test_broken_tables_lengths_and_starts_stay_in_bounds(kv_host, name):
         got = rd("k_out", np.float16, want[0].shape).astype(np.float64)
         assert np.all(np.abs(got - want[0]) <= np.abs(want[0]) * 2.0**-10.99 + 2.0**-25)
         assert int(rd("info", np.int32)[0]) == int(bad)
-    for hq in (4, 66):  # 66: the prompts' kernel
+    for hq, min_rows in ((4, -1), (66, 1)):  # the latter: the prompts' kernel
         qf, qs = C.cast(rng.standard_normal((4, hq, 64)), "f16")
         rd = run(kv_host, f"ba{hq}{name}", "attend", cache, table, lens, starts, 4, ld=hq * 64, ld_out=hq * 64, q_heads=hq,
-                 scale=0.125, q=qs)
+                 scale=0.125, q=qs, min_rows=min_rows)
         if not ordered:
             continue
         if lens.max() < 10**5:
