@@ -12,7 +12,7 @@ constexpr int ATT_WAVES = 4;
 constexpr int ATT_ROWS = 16;                     // query rows of a wave's MFMA
 constexpr int ATT_TILE = 32;                     // keys a wave takes at a time
 constexpr int ATT_MIN_CHUNK = 256;               // fewest keys of a workgroup when a row's keys are split
-constexpr int ATT_UNSPLIT = 512;                 // a table of at most so many keys is not split: a join costs 3 us
+constexpr int ATT_UNSPLIT = 512;                 // see cut_call
 constexpr int ATT_MAX_TARGET = 4 * 256;          // most workgroups that the keys are split for (Seq)
 constexpr int PROMPT_TARGET = 256;               // and in the prompts' kernel
 constexpr float ATT_W_TOP = 8.0f;                // log2 of the largest weight after a rescaling

@@ -8,11 +8,12 @@
 // 16-row block is one side of v_mfma_f32_16x16x32_f16, the keys or the head
 // dimension the other. With fewer rows (a head of its own, one token) the
 // spare columns cost matrix-core time that is free here, since the product
-// is bound by the cache's bytes and by their conversion.
+// is bound by the cache's bytes and by their conversion. Calls with very many
+// rows go to the prompts' kernel (kv_prompt.hip).
 //
 // Operands. The codes enter the MFMAs as integers: a 4-bit code c, moved to
-// bits 6..9 of an fp16 half and OR-ed under the exponent of 16, is 16 + c
-// exactly; an 8-bit one under the exponent of 1024 is 1024 + c. Scales and
+// bits 4..7 of an fp16 half and OR-ed under the exponent of 64, is 64 + c
+// exactly (bits 6..9 and 16 + c would take a fourth shift a word); an 8-bit one under the exponent of 1024 is 1024 + c. Scales and
 // zeros stay outside:
 //   S[key][row] = s_k (sum_d (off + c) q - (off + z_k) sum_d q)   (fp32)
 //   O[d][row]   = sum_key (c - z_v) w,  w = p s_v                 (c - z exact in fp16)
@@ -35,8 +36,19 @@
 //
 // Split. A workgroup's 4 waves take 32-key tiles in turn and are joined
 // through LDS; where the rows alone do not fill the GPU, a row block's keys
-// are split over workgroups too, whose partial sums kv_join adds in a fixed
-// order. Each partial result has its M; all reductions are fp32.
+// are split over workgroups too (Seq in kv_attention.h), whose partial sums
+// kv_join adds in a fixed order. Each partial result has its M; all
+// reductions are fp32.
+//
+// Measured (one MI355X, whose large copy runs at 5.1 TB/s): 24 sequences of
+// 2048 tokens, 96 heads of 128, 4 bits: 127 us, 5.1 TB/s of codes and grids;
+// there the VALU is 67% busy with 340 instructions a tile (64 conversions for
+// the keys, 96 for the values, 100 for the softmax). 64 ragged sequences of up
+// to 8192 tokens, 8 heads, 8 bits: 73 us (3.7 TB/s). One of 131072 tokens, 8
+// heads for 64, 4 bits: 41 us (3.5 TB/s): 33 us of streaming, of which 9 are the
+// chain length -> page -> codes and the tail, then the join. One short sequence:
+// 5.5 us up to 128 tokens, 1.3 us for each 128 more. Two tiles in flight a wave
+// (at 2 waves a SIMD instead of 3) were slower, 144 against 136 us on the first.
 #include "kv_attention.h"
 
 namespace gptq {
@@ -516,8 +528,16 @@ Cut cut_call(const KvCache& c, const KvBatch& b, int ratio, int64_t prompt_min_r
   static_assert(PROMPT_BLOCK == 1 << 7 && ATT_ROWS == 1 << 4, "rows of a row block");
   k.rows = b.starts || ratio > 1 << k.block_shift ? 1 << k.block_shift : ratio;
   k.blocks = b.starts ? row_blocks(b.n_tokens, ratio, k.block_shift) + b.batch : b.batch * row_blocks(1, ratio, k.block_shift);
-  const int64_t keys = b.max_pages << c.shift;
-  k.chunks = keys <= ATT_UNSPLIT ? 1 : (keys + ATT_MIN_CHUNK - 1) / ATT_MIN_CHUNK;
+  // Splitting costs a join (3 us in a table of up to 512 keys, against 2.6 us
+  // for the keys) and a plan over the whole batch in every workgroup. With 1024
+  // row blocks the GPU is full without it; then only a long table pays for the
+  // balance that it brings to ragged lengths (us, split and not, 4 bits):
+  // 1024 row blocks 2000 keys 41 / 35, 12000 keys 130 / 184; 2048 row blocks
+  // 8000 keys 187 / 193, 12000 keys 329 / 286, 20000 keys 335 / 379; 8192 row
+  // blocks 2000 keys 296 / 180.
+  const int64_t keys = b.max_pages << c.shift, full = k.blocks * c.heads;
+  const bool whole = keys <= ATT_UNSPLIT || (full >= 1024 && keys < 8 * full);
+  k.chunks = whole ? 1 : (keys + ATT_MIN_CHUNK - 1) / ATT_MIN_CHUNK;
   const int64_t parts = 2 * (k.prompt ? PROMPT_TARGET : ATT_MAX_TARGET) / c.heads + 2;
   k.parts = k.chunks <= 1 ? 0 : parts / k.chunks < k.blocks ? parts : k.blocks * k.chunks;
   return k;

@@ -20,6 +20,13 @@
 // within 2^-29 of a rounding boundary, so it is the correctly rounded one.
 // Residuals are exact while s is above 2^-90; smaller ones are scaled up.
 //
+// Measured (large copy 5.1 TB/s): 65536 tokens of 32 heads of 128, 8 bits, read
+// back to bf16 in 311 us (5.2 TB/s); 39680 tokens of 32 heads of 80, 4 bits, from
+// bf16 stored in 138 to 158 us (3.3 to 3.8 TB/s, the 16-lane rows of the range
+// hold 10 busy lanes) and read back in 135 us; 2048 tokens of 96 heads, 8 bits,
+// stored in 38 us (4.0 TB/s). A token: 3 us, the launch and three dependent
+// loads (length, page, place).
+//
 // q' + 1.5 * 2^23 is rint(q') in its low bits; those are clamped as floats and
 // gathered by shift-and-add, the zero point and the constant's own bits once
 // for all of a word's codes.

@@ -101,7 +101,7 @@ def attention_bound(ref, mag, q, cache, scale, slopes, q_dtype, out_dtype, longe
       twice. Its terms sum to at most `size` = scale * sum |q| * range of k (and the
       position bias); the matrix core rounds once for 4 products, so head_dim
       / 4 times; the one-part form adds the offset of the codes to its terms
-      (31 / 15 or 1279 / 255 of their range); scaling, bias, difference to the
+      (79 / 15 or 1279 / 255 of their range: offsets of 64 and 1024); scaling, bias, difference to the
       reference and the parts of q add up to 16 roundings more.
     * The sums over the keys: a wave of four takes every fourth tile, one
       rounding for 4 keys; joins and rescalings at most 300.
@@ -111,7 +111,7 @@ def attention_bound(ref, mag, q, cache, scale, slopes, q_dtype, out_dtype, longe
     size = abs(scale) * np.abs(q).sum(-1, keepdims=True) * span(cache, "k")
     if slopes is not None:
         size = size + np.abs(slopes)[None, :, None] * longest
-    offset = 1.0 if two else 31 / 15 if bits == 4 else 1279 / 255
+    offset = 1.0 if two else 79 / 15 if bits == 4 else 1279 / 255
     weight = 2.0**-22 if two else 2.0**-11
     scores = 2.0**-24 * size * offset * (dim / 4 + 16)
     sums = 2.0**-24 * (longest / 16 + 300)
