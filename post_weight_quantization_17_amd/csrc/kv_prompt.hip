@@ -13,12 +13,12 @@
 // of its rows sees.
 //
 // Measured: two causal prompts of 1500 and 976 tokens, 32 heads over 8 of 128,
-// 4 bits, 91 us with its idle join, 538 TFLOP/s of the 4.9e10 multiply-adds'
-// operations (a large fp16 matrix product runs at 1137). Instructions are issued
-// in 87% of the cycles (VALU 50%, scalar 19%, LDS 11%): 60 VALU operations for 32
-// keys of a row, of which the exponentials count fourfold, are twice the MFMAs'
-// time. Other layouts of the same work: 4 waves of two row tiles 125 us, 4 waves
-// of one 116, 64-row blocks whose waves halve the keys 134.
+// 4 bits, 91 us with an idle join: 538 TFLOP/s over the 4.9e10 operations that
+// the mask leaves (a large fp16 matrix product runs at 1137). Instructions are
+// issued in 87% of the cycles (VALU 50%, scalar 19%, LDS 11%); of the 60 VALU
+// operations for 32 keys of a row the 8 exponentials count fourfold. Other
+// layouts of the same work: 4 waves of two row tiles 125 us, 4 waves of one
+// 116, 64-row blocks whose waves halve the keys 134.
 #include "kv_attention.h"
 
 namespace gptq {
