@@ -449,7 +449,10 @@ int gptq_kv_cache_read(const gptq_kv_cache* cache, const gptq_kv_batch* batch, v
  * Sums and softmax statistics are fp32. Weights enter the second product as
  * fp16 with a common scale per row (error 2^-11 of a weight); with an fp32 q
  * or out both products take their operand in two fp16 parts (2^-22). Results
- * are deterministic. Queries that are not finite give NaN rows.
+ * are deterministic. Queries that are not finite give NaN rows. Grids of v
+ * whose step is below 2^-96 add an error of up to 2^-121 a key; with a step
+ * s > 2^100 of v, keys whose weight is below 2^-134 s of the row's largest may
+ * be left out.
  * Errors: the shared ones; q_heads < 1, > 65535 or no multiple of kv_heads,
  * ldq or ldo < q_heads * head_dim or > 2^40, NULL or unaligned q or out,
  * unaligned slopes or ws, scale not finite in fp32, unknown dtype, 2^24 or more

@@ -5,7 +5,6 @@
 
 #include "kv_cache.h"
 
-
 namespace gptq {
 
 constexpr int ATT_WAVES = 4;
@@ -17,6 +16,8 @@ constexpr int ATT_MAX_TARGET = 4 * 256;          // most workgroups that the key
 constexpr int PROMPT_TARGET = 256;               // and in the prompts' kernel
 constexpr float ATT_W_TOP = 8.0f;                // log2 of the largest weight after a rescaling
 constexpr float ATT_W_LIMIT = 32768.0f;          // a weight above this asks for the next one
+constexpr float ATT_S_LEAST = -96.0f;            // log2 of the least step of v that counts in M (kv_attention.hip)
+constexpr float ATT_SUM_LIMIT = 0x1p108f;        // a tile's sum of 2^(x - M) above this asks for a rescaling, too
 constexpr float ATT_LOWEST = -3.402823466e38f;   // M before the first key
 constexpr float LOG2E = 1.44269504088896340736f;
 

@@ -13,8 +13,8 @@
 //
 // Operands. The codes enter the MFMAs as integers: a 4-bit code c, moved to
 // bits 4..7 of an fp16 half and OR-ed under the exponent of 64, is 64 + c
-// exactly (bits 6..9 and 16 + c would take a fourth shift a word); an 8-bit one under the exponent of 1024 is 1024 + c. Scales and
-// zeros stay outside:
+// exactly (bits 6..9 and 16 + c would take a fourth shift a word); an 8-bit
+// one under the exponent of 1024 is 1024 + c. Scales and zeros stay outside:
 //   S[key][row] = s_k (sum_d (off + c) q - (off + z_k) sum_d q)   (fp32)
 //   O[d][row]   = sum_key (c - z_v) w,  w = p s_v                 (c - z exact in fp16)
 // No step rounds a dequantised value. The scores leave the first product
@@ -29,7 +29,9 @@
 // w = 2^(x - M) s_v goes to fp16, l = sum 2^(x - M) stays fp32. M is chosen so
 // that the largest w is 2^8 and moves only when some w passes 2^15, which
 // keeps w at full fp16 precision from 2^-22 of the largest on and lets most
-// tiles skip the rescaling. Queries are scaled to a largest element of 2^13
+// tiles skip the rescaling. Steps of v below 2^-96 count as 2^-96 there, since
+// the weights without them, 2^8 / s_v, would leave fp32; l stays below 2^127 for
+// 2^22 keys of such weights. Queries are scaled to a largest element of 2^13
 // to 2^14, exact for 16-bit types (bf16's exponents do not fit fp16); the
 // power of two is put back in fp32. fp32 queries, and weights for fp32
 // outputs, are split into two fp16 parts, each with its own MFMA.
@@ -273,10 +275,10 @@ kv_attend(AttArgs a) {
       w[e] = p * sv[e];
       big = fmaxf(big, w[e]);
     }
-    if (__any(big > ATT_W_LIMIT)) {
+    if (__any(big > ATT_W_LIMIT || sum > ATT_SUM_LIMIT)) {
       float top = ATT_LOWEST;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, x[e] + __builtin_amdgcn_logf(sv[e]) - ATT_W_TOP);
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, x[e] + fmaxf(__builtin_amdgcn_logf(sv[e]), ATT_S_LEAST) - ATT_W_TOP);
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       top = fmaxf(top, M);
@@ -368,7 +370,7 @@ kv_attend(AttArgs a) {
         product(4 * vw + 3, h);
       }
     }
-      if (more) load_values(at);
+    if (more) load_values(at);
     p0 += step;
   }
 

@@ -261,10 +261,10 @@ kv_attend_rows(AttArgs a) {
       w[e] = p * s[e];
       big = fmaxf(big, w[e]);
     }
-    if (__any(big > ATT_W_LIMIT)) {
+    if (__any(big > ATT_W_LIMIT || sum > ATT_SUM_LIMIT)) {
       float top = ATT_LOWEST;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, x[e] + __builtin_amdgcn_logf(s[e]) - ATT_W_TOP);
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, x[e] + fmaxf(__builtin_amdgcn_logf(s[e]), ATT_S_LEAST) - ATT_W_TOP);
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       top = fmaxf(top, M);

@@ -68,6 +68,20 @@ def cache(rng, n_pages, heads, page, dim, bits, garbage=False):
     return c
 
 
+# Values far from 1, as v = factor (3 + N(0, 1)), with the same weight for
+# every key. The smaller factor is above the bound's least error of longest *
+# 2^-121 by far. (head_dim, bits, q dtype, out dtype, factor)
+FAR_VALUES = [(64, 4, "bf16", "bf16", 2.0**-110), (64, 8, "f32", "f32", 2.0**-110), (64, 4, "f32", "f32", 2.0**100),
+              (64, 8, "bf16", "bf16", 2.0**100)]
+
+
+def far_cache(rng, n_pages, heads, page, dim, bits, factor):
+    c = cache(rng, n_pages, heads, page, dim, bits)
+    codes, c["v_grid"] = K.quantize(factor * (3 + rng.standard_normal((n_pages, heads, page, dim))), bits)
+    c["v_codes"] = K.pack(codes, bits)
+    return c
+
+
 def poison(c, table, lens):
     """Every place past a sequence's length, and every page that no sequence
     has, gets a NaN or infinite scale and all code bits set."""
@@ -96,7 +110,10 @@ def attention_bound(ref, mag, q, cache, scale, slopes, q_dtype, out_dtype, longe
 
     * A weight is rounded to fp16: 2^-11 of it (two parts: 2^-22). One below
       fp16's normal range is off by at most 2^-25 while the largest is at
-      least 2^8: 2^-33 of the range of v a key.
+      least 2^8: 2^-33 of the range of v a key. Steps of v below 2^-96 count
+      as that when the reference is chosen (so that 2^(x - M) stays finite):
+      the sum of the weights is then at least 2^(8 + 96), a key is off by at
+      most 2^-25 (2^bits - 1) over that.
     * A score's error moves its weight by as much, numerator and denominator:
       twice. Its terms sum to at most `size` = scale * sum |q| * range of k (and the
       position bias); the matrix core rounds once for 4 products, so head_dim
@@ -115,5 +132,6 @@ def attention_bound(ref, mag, q, cache, scale, slopes, q_dtype, out_dtype, longe
     weight = 2.0**-22 if two else 2.0**-11
     scores = 2.0**-24 * size * offset * (dim / 4 + 16)
     sums = 2.0**-24 * (longest / 16 + 300)
-    return (mag * (weight + 2 * scores + sums) + longest * 2.0**-33 * span(cache, "v")
+    reach = max(span(cache, "v"), (2**bits - 1) * 2.0**-96)
+    return (mag * (weight + 2 * scores + sums) + longest * 2.0**-33 * reach
             + np.abs(ref) * EPS[out_dtype] * 1.01 + TINY[out_dtype])

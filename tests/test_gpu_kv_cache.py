@@ -170,6 +170,19 @@ def test_attention(gpu, case):
     assert int(dev.info.item()) == 0
 
 
+@pytest.mark.parametrize("case", range(len(C.FAR_VALUES)))
+def test_attention_over_values_far_from_one(gpu, case):
+    dim, bits, qdt, odt, factor = C.FAR_VALUES[case]
+    rng = np.random.default_rng(300 + case)
+    for n, hq in ((3, 2), (400, 128)):  # the latter: the prompts' kernel
+        table, lens, starts, n_pages = C.batch(rng, [n + 147], [n], 16)
+        cache = C.far_cache(rng, n_pages, 1, 16, dim, bits, factor)
+        qf, _ = C.cast(rng.standard_normal((n, hq, dim)), qdt)
+        got = gpu.gptq_kv_attention(dense(qf, qdt), upload(gpu, cache), up(table), up(lens), starts=up(starts), scale=0.0,
+                                    dtype=TORCH[odt])
+        check_attention(got, qf, cache, table, lens, starts, 0.0, None, qdt, odt)
+
+
 def test_many_sequences(gpu):
     """More sequences than a wave has lanes, most of them short, one long:
     the plan's passes over the batch, units of the long one joined."""

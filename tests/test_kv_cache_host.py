@@ -219,6 +219,23 @@ def test_attention_runs_in_bounds_and_matches_the_oracle(kv_host, case):
     assert np.all(err <= bound), float(np.max(err / bound))
 
 
+@pytest.mark.parametrize("min_rows", [-1, 1])  # 1: the prompts' kernel
+@pytest.mark.parametrize("case", range(len(C.FAR_VALUES)))
+def test_attention_over_values_far_from_one(kv_host, case, min_rows):
+    dim, bits, qdt, odt, factor = C.FAR_VALUES[case]
+    rng = np.random.default_rng(300 + case)
+    table, lens, starts, n_pages = C.batch(rng, [150], [3], 16)
+    cache = C.far_cache(rng, n_pages, 1, 16, dim, bits, factor)
+    qf, qs = C.cast(rng.standard_normal((3, 2, dim)), qdt)
+    rd = run(kv_host, f"f{case}{min_rows}", "attend", cache, table, lens, starts, 3, dtype=qdt, out_dtype=odt, ld=2 * dim,
+             ld_out=2 * dim, q_heads=2, scale=0.0, q=qs, min_rows=min_rows)
+    ref, mag, _, _ = K.attention(qf, cache, table, lens, starts, 0.0)
+    got, _ = rows(rd("out", STORAGE[odt]), 3, 2 * dim, 2 * dim, odt)
+    bound = C.attention_bound(ref, mag, qf, cache, 0.0, None, qdt, odt, 150)
+    assert np.all(bound < np.abs(ref).max() / 16)
+    assert np.all(np.abs(got.reshape(ref.shape) - ref) <= bound)
+
+
 BROKEN = [
     ("pages", dict(entry=1000)),
     ("pages_negative", dict(entry=-1)),
