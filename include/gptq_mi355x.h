@@ -455,9 +455,10 @@ int gptq_kv_cache_read(const gptq_kv_cache* cache, const gptq_kv_batch* batch, v
  * be left out.
  * Errors: the shared ones; q_heads < 1, > 65535 or no multiple of kv_heads,
  * ldq or ldo < q_heads * head_dim or > 2^40, NULL or unaligned q or out,
- * unaligned slopes or ws, scale not finite in fp32, unknown dtype, 2^24 or more
- * workgroups (kv_heads times the 16-row blocks of the call's query rows) ->
- * GPTQ_E_INVALID_ARG; ws_bytes too small -> GPTQ_E_WORKSPACE. The workspace
+ * unaligned slopes or ws, scale not finite in fp32, unknown dtype, about 2^28 or
+ * more query rows (kv_heads times the sequences' new tokens times q_heads /
+ * kv_heads, each sequence's in whole blocks of 16; prompts: 2^30, in blocks of
+ * 128) -> GPTQ_E_INVALID_ARG; ws_bytes too small -> GPTQ_E_WORKSPACE. The workspace
  * size is 0 for arguments that would be refused. */
 size_t gptq_kv_attention_workspace_size(const gptq_kv_cache* cache, const gptq_kv_batch* batch, int64_t q_heads);
 int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const void* q, int q_dtype,

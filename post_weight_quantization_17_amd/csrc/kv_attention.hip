@@ -605,7 +605,8 @@ int attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const void
   const int dp = a.c.dim <= 64 ? 64 : a.c.dim <= 128 ? 128 : 256;
   a.target = k.prompt ? PROMPT_TARGET : 256 * att_waves_per_simd(cache->bits, dp, split);
   const int64_t units = call_units(k, a.c.heads, a.target);
-  if (units * a.c.heads >= (int64_t(1) << 24)) return GPTQ_E_INVALID_ARG;
+  // A launch has fewer than 2^32 threads (256 a workgroup, 512 in the prompts' kernel).
+  if (units * a.c.heads >= (int64_t(1) << (k.prompt ? 23 : 24))) return GPTQ_E_INVALID_ARG;
   a.block_shift = k.block_shift;
   a.by_heads = Divider::by(uint32_t(a.c.heads));
   a.by_ratio = Divider::by(uint32_t(a.ratio));

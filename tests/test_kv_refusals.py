@@ -102,6 +102,9 @@ def test_attention_refusals(lib):
     # more workgroups than a launch holds
     assert attend(lib, cache={"kv_heads": 1, "head_dim": 16}, batch={"batch": 2**25, "n_tokens": 2**25}, heads=1, ldq=16,
                   ldo=16) == BAD
+    # the same for prompts, whose workgroups are twice as large: 2^23 blocks of 128 rows
+    assert attend(lib, cache={"kv_heads": 1, "head_dim": 16}, batch={"starts": P, "batch": 1, "n_tokens": 2**24}, heads=64,
+                  ldq=1024, ldo=1024) == BAD
 
 
 def test_workspace_refusals(lib):
