@@ -685,8 +685,8 @@ def gptq_kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens
     attention of q [n_tokens, q_heads, head_dim] (fp16, bf16 or fp32) over
     the cached tokens of its sequences, its own among them. ``scale``: by
     default 1 / sqrt(head_dim); ``slopes`` fp32 [q_heads]: linear position
-    biases. Rows past ``starts[batch]`` are left as they are (unspecified in
-    a new tensor)."""
+    biases. ``out`` must not overlap q. Rows past ``starts[batch]`` are left
+    as they are (unspecified in a new tensor)."""
     index = cache._index
     if q.dim() != 3 or q.shape[1] < 1 or q.shape[1] % cache._heads != 0:
         raise ValueError("q must be [n_tokens, q_heads, head_dim], its heads a multiple of the cache's")

@@ -47,9 +47,9 @@
 // there the VALU is 67% busy with 340 instructions a tile (64 conversions for
 // the keys, 96 for the values, 100 for the softmax). 64 ragged sequences of up
 // to 8192 tokens, 8 heads, 8 bits: 73 us (3.7 TB/s). One of 131072 tokens, 8
-// heads for 64, 4 bits: 41 us (3.5 TB/s): 33 us of streaming, of which 9 are the
-// chain length -> page -> codes and the tail, then the join. One short sequence:
-// 5.5 us up to 128 tokens, 1.3 us for each 128 more. Two tiles in flight a wave
+// heads for 64, 4 bits: 41 us (3.5 TB/s): 35 us here, against 28 for the bytes
+// alone (the chain length -> page -> codes and the tail), then the join. One short
+// sequence, replayed in a graph: 5.5 us up to 128 tokens, 6.9 up to 256. Two tiles in flight a wave
 // (at 2 waves a SIMD instead of 3) were slower, 144 against 136 us on the first.
 #include "kv_attention.h"
 

@@ -13,7 +13,7 @@
 // of its rows sees.
 //
 // Measured: two causal prompts of 1500 and 976 tokens, 32 heads over 8 of 128,
-// 4 bits, 91 us with an idle join: 538 TFLOP/s over the 4.9e10 operations that
+// 4 bits, 92 us with an idle join: 534 TFLOP/s over the 4.9e10 operations that
 // the mask leaves (a large fp16 matrix product runs at 1137). Instructions are
 // issued in 87% of the cycles (VALU 50%, scalar 19%, LDS 11%); of the 60 VALU
 // operations for 32 keys of a row the 8 exponentials count fourfold. Other
