@@ -459,7 +459,8 @@ int gptq_kv_cache_read(const gptq_kv_cache* cache, const gptq_kv_batch* batch, v
  * more query rows (kv_heads times the sequences' new tokens times q_heads /
  * kv_heads, each sequence's in whole blocks of 16; prompts: 2^30, in blocks of
  * 128) -> GPTQ_E_INVALID_ARG; ws_bytes too small -> GPTQ_E_WORKSPACE. The workspace
- * size is 0 for arguments that would be refused. */
+ * size is 0 for a cache, a batch or q_heads that would be refused (the number of
+ * query rows aside). */
 size_t gptq_kv_attention_workspace_size(const gptq_kv_cache* cache, const gptq_kv_batch* batch, int64_t q_heads);
 int gptq_kv_attention(const gptq_kv_cache* cache, const gptq_kv_batch* batch, const void* q, int q_dtype,
                       int64_t q_heads, int64_t ldq, double scale, const float* slopes, void* out, int out_dtype,

@@ -573,7 +573,7 @@ size_t attention_workspace(const gptq_kv_cache* cache, const gptq_kv_batch* batc
                            int64_t prompt_min_rows) {
   KvCache c;
   KvBatch b;
-  if (kv_views(cache, batch, &c, &b) != GPTQ_OK || q_heads < 1 || q_heads % c.heads != 0) return 0;
+  if (kv_views(cache, batch, &c, &b) != GPTQ_OK || q_heads < 1 || q_heads > 65535 || q_heads % c.heads != 0) return 0;
   if (b.batch == 0 || b.n_tokens == 0) return 0;
   const Cut k = cut_call(c, b, int(q_heads / c.heads), prompt_min_rows);
   return size_t(k.parts) * size_t(c.heads) * size_t(k.rows) * (size_t(c.dim) * sizeof(float) + sizeof(float2));

@@ -124,6 +124,13 @@ def test_workspace_refusals(lib):
     assert lib.gptq_kv_attention_workspace_size(c, b, 4) == need
 
 
+def test_workspace_size_of_refused_head_counts(lib):
+    c, b = structs({}, {"ld_table": 2**20, "max_pages": 2**20})
+    assert lib.gptq_kv_attention_workspace_size(c, b, 65534) > 0
+    for heads in (0, -2, 3, 65536, 2**33):
+        assert lib.gptq_kv_attention_workspace_size(c, b, heads) == 0, heads
+
+
 def test_empty_calls_do_nothing(lib):
     none = {"batch": 0, "n_tokens": 0, "table": None, "lens": None}
     assert dense(lib, batch=none, k=None, v=None) == OK
